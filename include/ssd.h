@@ -440,6 +440,43 @@ ssd_status ssd_causal_conv1d(const ssd_conv1d_args* args, void* stream);
  * (the flag is cleared), else SSD_OK. */
 ssd_status ssd_conv1d_check_status(void* stream);
 
+/* Gradients of ssd_causal_conv1d: of J = sum dy . y + d_final : final_state
+ * with respect to x, weight, bias and init_state.  With o the sum before the
+ * activation (recomputed here) and do = dy silu'(o) (dy without activation),
+ *   dxin[i] = sum_k w[c, k] do[i + (K-1) - k],  dweight[c, k] = sum_t do[t] xin[t-(K-1)+k],
+ *   dbias[c] = sum_t do[t]
+ * where dxin covers x and, before it, the carried inputs (d_init).  Sums over
+ * time and batch are fp32 and run in a fixed order: repeated calls give
+ * bitwise-identical results.
+ * Layouts: x, dy, dx [batch, seqlen, channels] dtype; weight, dweight
+ *   [channels, width], bias, dbias [channels], init_state, d_init, d_final
+ *   [batch, channels, width - 1] fp32; bias, init_state, d_final NULL = 0;
+ *   dbias, d_init NULL = not written.
+ * Supported: as ssd_causal_conv1d, and seqlen < 2^31; x, dy, dx and the
+ *   workspace 16-byte aligned.  dx must not overlap x or dy. */
+typedef struct {
+    int64_t batch, seqlen, channels, width;
+    int32_t dtype;
+    int32_t activation;     /* 1 = SiLU, 0 = none */
+    const void* x;
+    const float* weight;
+    const float* bias;
+    const float* init_state;
+    const void* dy;
+    const float* d_final;
+    void* dx;
+    float* dweight;
+    float* dbias;
+    float* d_init;
+    void* workspace;        /* device scratch, >= ssd_causal_conv1d_bwd_workspace_size() */
+    size_t workspace_bytes;
+} ssd_conv1d_bwd_args;
+
+/* Bytes of workspace for these sizes (0 if invalid or unsupported). */
+size_t ssd_causal_conv1d_bwd_workspace_size(const ssd_conv1d_bwd_args* args);
+
+ssd_status ssd_causal_conv1d_bwd(const ssd_conv1d_bwd_args* args, void* stream);
+
 /* One decode step of the same convolution (its half of the Mamba2Cache):
  * state [batch, channels, width - 1] fp32 holds the previous width - 1 inputs,
  * oldest first, and is shifted in place to end with x;
@@ -460,6 +497,182 @@ typedef struct {
 } ssd_conv1d_update_args;
 
 ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
+
+/* ---- gated linear recurrence ------------------------------------------------ */
+/* An elementwise recurrence whose decay and input weight are gated by the
+ * token (the gated linear recurrent unit of the literature), one state per
+ * channel:
+ *   r_t = sigma(gate_a_t),  i_t = sigma(gate_x_t),  sigma(v) = 1 / (1 + e^-v)
+ *   log a_t = -scale softplus(decay_c) r_t
+ *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t;   y_t = h_t
+ * Where reset is nonzero a token starts a new sequence: a_t = 0, so h_t =
+ * i_t x_t (packed documents; at token 0 it drops init_state).
+ * Layouts: x, gate_a, gate_x, y [batch, seqlen, channels] dtype; decay
+ *   [channels] fp32; reset [batch, seqlen] bytes or NULL (= none);
+ *   init_state, final_state [batch, channels] fp32 or NULL (= 0 / not
+ *   returned); states [batch, ceil(seqlen / SSD_GATED_SCAN_INTERVAL),
+ *   channels] fp32 or NULL: receives the state before tokens 0, 64, 128, ...
+ *   (states[:, 0] = init_state), which ssd_gated_scan_bwd takes.
+ * Gates, decays and the carried state are fp32 for both types; y is the fp32
+ * state rounded once.  Results do not depend on timing (no atomics).
+ * Supported: channels a multiple of 8 (bf16) or 4 (fp32), batch <= 65535,
+ *   seqlen < 2^31 (else SSD_ERR_UNSUPPORTED); scale > 0 and finite; every
+ *   pointer but reset 16-byte aligned (else SSD_ERR_INVALID_ARG).  Outputs
+ *   must not overlap inputs. */
+#define SSD_GATED_SCAN_INTERVAL 64
+typedef struct {
+    int64_t batch, seqlen, channels;
+    int32_t dtype;
+    float scale;
+    const void* x;
+    const void* gate_a;
+    const void* gate_x;
+    const float* decay;
+    const uint8_t* reset;
+    const float* init_state;
+    void* y;
+    float* final_state;
+    float* states;
+} ssd_gated_scan_args;
+
+ssd_status ssd_gated_scan(const ssd_gated_scan_args* args, void* stream);
+
+/* Gradients of ssd_gated_scan: of J = sum dy . y + d_final . h_L with respect to
+ * x, gate_a, gate_x, decay and init_state.  `states` is the forward's (same
+ * inputs); h is recomputed from it inside each 64-token interval.  With the
+ * adjoint g_t = dy_t + a_{t+1} g_{t+1} (g_L + d_final), n_t = sqrt(1 - a_t^2)
+ * and la_t = log a_t,
+ *   dx = g n i;  dgate_x = g n x i (1 - i);
+ *   dla = g (a h_{t-1} - a^2 / n i x);  dgate_a = dla la (1 - r);
+ *   ddecay = -scale sigma(decay) sum dla r;  d_init = a_1 g_1.
+ * A reset token passes nothing to gate_a, decay or the state before it.
+ * dgate_a, dgate_x, dx: dtype; d_final [batch, channels] fp32 or NULL (= 0);
+ * ddecay [channels], d_init [batch, channels] fp32, d_init NULL = not written.
+ * Sums over time and batch are fp32 in a fixed order (bitwise repeatable).
+ * Supported, alignment and errors as for ssd_gated_scan. */
+typedef struct {
+    int64_t batch, seqlen, channels;
+    int32_t dtype;
+    float scale;
+    const void* x;
+    const void* gate_a;
+    const void* gate_x;
+    const float* decay;
+    const uint8_t* reset;
+    const float* states;
+    const void* dy;
+    const float* d_final;
+    void* dx;
+    void* dgate_a;
+    void* dgate_x;
+    float* ddecay;
+    float* d_init;
+    void* workspace;        /* device scratch, >= ssd_gated_scan_bwd_workspace_size() */
+    size_t workspace_bytes;
+} ssd_gated_scan_bwd_args;
+
+/* Bytes of workspace for these sizes (0 if invalid or unsupported). */
+size_t ssd_gated_scan_bwd_workspace_size(const ssd_gated_scan_bwd_args* args);
+
+ssd_status ssd_gated_scan_bwd(const ssd_gated_scan_bwd_args* args, void* stream);
+
+/* One decode step of the same recurrence: state [batch, channels] fp32 ->
+ * new_state (which may be state: in place; or another buffer, keeping the
+ * state to return to when a drafted token is rejected); x, gate_a, gate_x, y
+ * [batch, channels] dtype; reset [batch] bytes or NULL.  Supported and errors
+ * as for ssd_gated_scan.  Consecutive calls on one stream go out with
+ * programmatic dependent launch. */
+typedef struct {
+    int64_t batch, channels;
+    int32_t dtype;
+    float scale;
+    const float* state;
+    const void* x;
+    const void* gate_a;
+    const void* gate_x;
+    const float* decay;
+    const uint8_t* reset;
+    float* new_state;
+    void* y;
+} ssd_gated_state_update_args;
+
+ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* args, void* stream);
+
+/* ---- head norm with the position rotation ----------------------------------- */
+/* RMSNorm over each head of the queries and keys (C and B in the scan's dual
+ * form) and the rotation of their leading elements by the token's position, in
+ * one pass.  For a head v of `headdim` elements with weight w:
+ *   u = v / sqrt(mean(v^2) + eps) * w
+ *   out_a = u_a cos f - u_b sin f,  out_b = u_a sin f + u_b cos f,
+ *   f = position * inv_freq[j],  j < rot_dim / 2
+ * for the pairs (a, b) = (j, j + rot_dim / 2), or (2j, 2j + 1) with `adjacent`;
+ * elements from rot_dim on are not rotated.  The angle is formed in fp64 and
+ * reduced by whole turns before its cosine and sine (fp32).
+ * Layouts: q, q_out: batch * seqlen tokens q_stride / q_out_stride elements
+ *   apart, each with q_heads dense heads of headdim elements, dtype; k, k_out
+ *   alike (NULL with k_heads = 0).  So slices of one packed row per token are
+ *   read and written in place.  q_weight, k_weight [headdim] fp32 or NULL (= 1);
+ *   inv_freq [rot_dim / 2] fp32 (NULL with rot_dim = 0); positions [batch,
+ *   seqlen] int64 or NULL (= 0, 1, ... in each batch row).
+ *   q_out may be q with the same stride (in place), k_out k likewise; nothing
+ *   else may overlap.
+ * Supported: headdim a multiple of 8, <= 256; rot_dim a multiple of 16, <=
+ *   headdim; strides a multiple of 8 (bf16) or 4 (fp32) elements; q_heads >= 1,
+ *   k_heads >= 0; q_heads + k_heads <= 65536; batch * seqlen < 2^31 (else
+ *   SSD_ERR_UNSUPPORTED); strides >= heads * headdim; eps >= 0 and finite;
+ *   pointers 16-byte aligned (positions: 8) (else SSD_ERR_INVALID_ARG). */
+typedef struct {
+    int64_t batch, seqlen, q_heads, k_heads, headdim, rot_dim;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    int32_t dtype;
+    int32_t adjacent;       /* 1 = rotate pairs (2j, 2j + 1), 0 = (j, j + rot_dim / 2) */
+    float eps;
+    const void* q;
+    const void* k;
+    const float* q_weight;
+    const float* k_weight;
+    const float* inv_freq;
+    const int64_t* positions;
+    void* q_out;
+    void* k_out;
+} ssd_qk_norm_rope_args;
+
+ssd_status ssd_qk_norm_rope(const ssd_qk_norm_rope_args* args, void* stream);
+
+/* Gradients of ssd_qk_norm_rope.  With e the incoming gradient rotated back (by
+ * -f), s = 1 / sqrt(mean(v^2) + eps):
+ *   dv = s (e w - v s^2 mean(e w v));  dweight = sum over tokens and heads of e v s.
+ * The sums are fp32 and run in a fixed order (bitwise repeatable).
+ * dq_out, dk_out and dq, dk: as q, k with the strides named after them;
+ * dq_weight, dk_weight [headdim] fp32 or NULL (not written); q and dq_out may
+ * have any strides allowed above, dq must not overlap the inputs.
+ * Supported, alignment and errors as for ssd_qk_norm_rope. */
+typedef struct {
+    int64_t batch, seqlen, q_heads, k_heads, headdim, rot_dim;
+    int64_t q_stride, k_stride, dq_out_stride, dk_out_stride, dq_stride, dk_stride;
+    int32_t dtype;
+    int32_t adjacent;
+    float eps;
+    const void* q;
+    const void* k;
+    const float* q_weight;
+    const float* k_weight;
+    const float* inv_freq;
+    const int64_t* positions;
+    const void* dq_out;
+    const void* dk_out;
+    void* dq;
+    void* dk;
+    float* dq_weight;
+    float* dk_weight;
+    void* workspace;        /* device scratch, >= ssd_qk_norm_rope_bwd_workspace_size() */
+    size_t workspace_bytes;
+} ssd_qk_norm_rope_bwd_args;
+
+/* Bytes of workspace for these sizes (0 if invalid or unsupported). */
+size_t ssd_qk_norm_rope_bwd_workspace_size(const ssd_qk_norm_rope_bwd_args* args);
+
+ssd_status ssd_qk_norm_rope_bwd(const ssd_qk_norm_rope_bwd_args* args, void* stream);
 
 /* ---- gated RMSNorm (after the scan) ------------------------------------- */
 /* The normalisation "MAMBA-2 Implementation Gaps" (section 7.3, items 9 and

@@ -9,6 +9,7 @@ raises immediately.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -28,6 +29,10 @@ __all__ = [
     "ssd_causal_conv1d", "ssd_conv1d_update", "ssd_conv1d_check_status",
     "ssd_bwd", "ssd_bwd_workspace_size", "ssd_selective_scan", "ssd_selective_scan_workspace_size",
     "ssd_selective_state_update", "ssd_gated_rmsnorm",
+    "ssd_causal_conv1d_bwd", "ssd_causal_conv1d_bwd_workspace_size",
+    "ssd_gated_scan", "ssd_gated_scan_bwd", "ssd_gated_scan_bwd_workspace_size",
+    "ssd_gated_state_update", "SSD_GATED_SCAN_INTERVAL",
+    "ssd_qk_norm_rope", "ssd_qk_norm_rope_bwd", "ssd_qk_norm_rope_bwd_workspace_size",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -41,6 +46,7 @@ SSD_FLAG_SPLIT_STEPS = 4
 SSD_FLAG_BF16_STATES = 8
 SSD_FLAG_SINGLE_PASS = 16
 SSD_TC_CHUNK_STATE, SSD_TC_CHUNK_SCAN, SSD_TC_FUSED = 1, 2, 4
+SSD_GATED_SCAN_INTERVAL = 64
 
 _i64, _i32, _vp, _sz = ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_size_t
 
@@ -108,6 +114,61 @@ class SsdGatedRmsnormArgs(ctypes.Structure):
     """Mirror of ssd_gated_rmsnorm_args."""
     _fields_ = [("rows", _i64), ("channels", _i64), ("group", _i64), ("dtype", _i32),
                 ("eps", ctypes.c_float), ("y", _vp), ("z", _vp), ("weight", _vp), ("out", _vp)]
+
+
+class SsdConv1dBwdArgs(ctypes.Structure):
+    """Mirror of ssd_conv1d_bwd_args."""
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("width", _i64),
+                ("dtype", _i32), ("activation", _i32), ("x", _vp), ("weight", _vp),
+                ("bias", _vp), ("init_state", _vp), ("dy", _vp), ("d_final", _vp), ("dx", _vp),
+                ("dweight", _vp), ("dbias", _vp), ("d_init", _vp), ("workspace", _vp),
+                ("workspace_bytes", _sz)]
+
+
+class SsdGatedScanArgs(ctypes.Structure):
+    """Mirror of ssd_gated_scan_args."""
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("dtype", _i32),
+                ("scale", ctypes.c_float), ("x", _vp), ("gate_a", _vp), ("gate_x", _vp),
+                ("decay", _vp), ("reset", _vp), ("init_state", _vp), ("y", _vp),
+                ("final_state", _vp), ("states", _vp)]
+
+
+class SsdGatedScanBwdArgs(ctypes.Structure):
+    """Mirror of ssd_gated_scan_bwd_args."""
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("channels", _i64), ("dtype", _i32),
+                ("scale", ctypes.c_float), ("x", _vp), ("gate_a", _vp), ("gate_x", _vp),
+                ("decay", _vp), ("reset", _vp), ("states", _vp), ("dy", _vp), ("d_final", _vp),
+                ("dx", _vp), ("dgate_a", _vp), ("dgate_x", _vp), ("ddecay", _vp),
+                ("d_init", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class SsdGatedStateUpdateArgs(ctypes.Structure):
+    """Mirror of ssd_gated_state_update_args."""
+    _fields_ = [("batch", _i64), ("channels", _i64), ("dtype", _i32), ("scale", ctypes.c_float),
+                ("state", _vp), ("x", _vp), ("gate_a", _vp), ("gate_x", _vp), ("decay", _vp),
+                ("reset", _vp), ("new_state", _vp), ("y", _vp)]
+
+
+class SsdQkNormRopeArgs(ctypes.Structure):
+    """Mirror of ssd_qk_norm_rope_args."""
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("q_heads", _i64), ("k_heads", _i64),
+                ("headdim", _i64), ("rot_dim", _i64), ("q_stride", _i64), ("k_stride", _i64),
+                ("q_out_stride", _i64), ("k_out_stride", _i64), ("dtype", _i32),
+                ("adjacent", _i32), ("eps", ctypes.c_float), ("q", _vp), ("k", _vp),
+                ("q_weight", _vp), ("k_weight", _vp), ("inv_freq", _vp), ("positions", _vp),
+                ("q_out", _vp), ("k_out", _vp)]
+
+
+class SsdQkNormRopeBwdArgs(ctypes.Structure):
+    """Mirror of ssd_qk_norm_rope_bwd_args."""
+    _fields_ = [("batch", _i64), ("seqlen", _i64), ("q_heads", _i64), ("k_heads", _i64),
+                ("headdim", _i64), ("rot_dim", _i64), ("q_stride", _i64), ("k_stride", _i64),
+                ("dq_out_stride", _i64), ("dk_out_stride", _i64), ("dq_stride", _i64),
+                ("dk_stride", _i64), ("dtype", _i32), ("adjacent", _i32),
+                ("eps", ctypes.c_float), ("q", _vp), ("k", _vp), ("q_weight", _vp),
+                ("k_weight", _vp), ("inv_freq", _vp), ("positions", _vp), ("dq_out", _vp),
+                ("dk_out", _vp), ("dq", _vp), ("dk", _vp), ("dq_weight", _vp),
+                ("dk_weight", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
 class SsdError(RuntimeError):
@@ -185,6 +246,24 @@ def load_library():
     lib.ssd_conv1d_update.argtypes = [ctypes.POINTER(SsdConv1dUpdateArgs), _vp]
     lib.ssd_gated_rmsnorm.restype = ctypes.c_int
     lib.ssd_gated_rmsnorm.argtypes = [ctypes.POINTER(SsdGatedRmsnormArgs), _vp]
+    lib.ssd_causal_conv1d_bwd.restype = ctypes.c_int
+    lib.ssd_causal_conv1d_bwd.argtypes = [ctypes.POINTER(SsdConv1dBwdArgs), _vp]
+    lib.ssd_causal_conv1d_bwd_workspace_size.restype = _sz
+    lib.ssd_causal_conv1d_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdConv1dBwdArgs)]
+    lib.ssd_gated_scan.restype = ctypes.c_int
+    lib.ssd_gated_scan.argtypes = [ctypes.POINTER(SsdGatedScanArgs), _vp]
+    lib.ssd_gated_scan_bwd.restype = ctypes.c_int
+    lib.ssd_gated_scan_bwd.argtypes = [ctypes.POINTER(SsdGatedScanBwdArgs), _vp]
+    lib.ssd_gated_scan_bwd_workspace_size.restype = _sz
+    lib.ssd_gated_scan_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdGatedScanBwdArgs)]
+    lib.ssd_gated_state_update.restype = ctypes.c_int
+    lib.ssd_gated_state_update.argtypes = [ctypes.POINTER(SsdGatedStateUpdateArgs), _vp]
+    lib.ssd_qk_norm_rope.restype = ctypes.c_int
+    lib.ssd_qk_norm_rope.argtypes = [ctypes.POINTER(SsdQkNormRopeArgs), _vp]
+    lib.ssd_qk_norm_rope_bwd.restype = ctypes.c_int
+    lib.ssd_qk_norm_rope_bwd.argtypes = [ctypes.POINTER(SsdQkNormRopeBwdArgs), _vp]
+    lib.ssd_qk_norm_rope_bwd_workspace_size.restype = _sz
+    lib.ssd_qk_norm_rope_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdQkNormRopeBwdArgs)]
     lib.ssd_conv1d_check_status.restype = ctypes.c_int
     lib.ssd_conv1d_check_status.argtypes = [_vp]
     lib.ssd_status_string.restype = ctypes.c_char_p
@@ -705,3 +784,294 @@ def ssd_gated_rmsnorm(y, z, weight, *, group: int | None = None, eps: float = 1e
     a.y, a.z, a.weight, a.out = _ptr(y), _ptr(z), _ptr(weight), _ptr(out)
     _check(lib.ssd_gated_rmsnorm(ctypes.byref(a), _stream_ptr(stream)), "ssd_gated_rmsnorm")
     return out
+
+
+# ---------------------------------------------------------------------------
+# The gated linear recurrence, the head norm with the position rotation and the
+# convolution's gradient.
+def _need(t, name, shape, dtype, like):
+    """t must have this shape and dtype and lie, dense, on like's device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    return _ptr(t)
+
+
+def _opt(t, name, shape, dtype, like):
+    return None if t is None else _need(t, name, shape, dtype, like)
+
+
+def _reset_ptr(reset, shape, like):
+    if reset is None:
+        return None
+    return _need(reset, "reset", shape, torch.bool if reset.dtype == torch.bool else torch.uint8, like)
+
+
+def _allocating_on(stream):
+    """Outputs and scratch come from the pool of the stream that writes them, so
+    that the allocator orders their reuse by that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _run(fn, a, stream, like):
+    """Calls the library function on the stream; like is one of the call's tensors."""
+    if not like.is_cuda:
+        raise SsdError(SSD_ERR_INVALID_ARG, fn.__name__ + " (host memory)")
+    _check(fn(ctypes.byref(a), _stream_ptr(stream)), fn.__name__)
+
+
+def _check_workspace(workspace, need, like):
+    if workspace.device != like.device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {like.device}")
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise ValueError(f"workspace has {have} bytes, {need} are needed")
+    return workspace.data_ptr(), have
+
+
+def ssd_causal_conv1d_bwd_workspace_size(batch, seqlen, channels, width, dtype=torch.bfloat16) -> int:
+    a = SsdConv1dBwdArgs(batch=batch, seqlen=seqlen, channels=channels, width=width,
+                         dtype=SSD_BF16 if dtype == torch.bfloat16 else SSD_F32)
+    return int(load_library().ssd_causal_conv1d_bwd_workspace_size(ctypes.byref(a)))
+
+
+def ssd_causal_conv1d_bwd(x, weight, dy, bias=None, init_state=None, d_final=None, *,
+                          activation: bool = True, out=None, workspace=None, stream=None) -> dict:
+    """Gradients of ssd_causal_conv1d: of sum(dy * y) + sum(d_final * final_state).
+    x, dy [b,L,C] in one dtype; weight [C,K], bias [C], init_state and d_final
+    [b,C,K-1] float32 (the last three optional).  Returns a dict dx (x's dtype),
+    dweight [C,K], dbias [C], d_init [b,C,K-1] (float32); ``out`` may hold
+    preallocated tensors under the same keys."""
+    lib = load_library()
+    b, L, Cn = x.shape
+    K = weight.shape[1]
+    f32 = torch.float32
+    state = (b, Cn, K - 1)
+    a = SsdConv1dBwdArgs(
+        batch=b, seqlen=L, channels=Cn, width=K, dtype=_dtype_code(x), activation=1 if activation else 0,
+        x=_ptr(x), weight=_need(weight, "weight", (Cn, K), f32, x), bias=_opt(bias, "bias", (Cn,), f32, x),
+        init_state=_opt(init_state, "init_state", state, f32, x) if K > 1 else None,
+        dy=_need(dy, "dy", x.shape, x.dtype, x),
+        d_final=_opt(d_final, "d_final", state, f32, x) if K > 1 else None)
+    need = int(lib.ssd_causal_conv1d_bwd_workspace_size(ctypes.byref(a)))
+    if need == 0:
+        raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_causal_conv1d_bwd (sizes)")
+    o = dict(out or {})
+    with _allocating_on(stream):
+        for name, shape, dtype in (("dx", x.shape, x.dtype), ("dweight", (Cn, K), f32),
+                                   ("dbias", (Cn,), f32), ("d_init", state, f32)):
+            if name not in o:
+                o[name] = torch.empty(shape, dtype=dtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    a.dx = _need(o["dx"], "dx", x.shape, x.dtype, x)
+    a.dweight = _need(o["dweight"], "dweight", (Cn, K), f32, x)
+    a.dbias = _need(o["dbias"], "dbias", (Cn,), f32, x)
+    a.d_init = _need(o["d_init"], "d_init", state, f32, x) if K > 1 else None
+    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, x)
+    _run(lib.ssd_causal_conv1d_bwd, a, stream, x)
+    return o
+
+
+def ssd_gated_scan(x, gate_a, gate_x, decay, init_state=None, reset=None, *, scale: float = 8.0,
+                   y=None, final_state=None, return_final_state: bool = False, states=None,
+                   return_states: bool = False, stream=None):
+    """The gated linear recurrence h_t = a_t h_{t-1} + sqrt(1 - a_t^2)
+    sigma(gate_x_t) x_t with log a_t = -scale softplus(decay) sigma(gate_a_t);
+    y_t = h_t.  x, gate_a, gate_x [b,L,C] in one dtype; decay [C] and init_state
+    [b,C] float32; reset [b,L] bool or uint8, nonzero where a token starts a new
+    sequence.  Returns y, then the final state [b,C] and the states entering
+    every 64th token [b,ceil(L/64),C] (for ssd_gated_scan_bwd), each when asked
+    for or given."""
+    lib = load_library()
+    b, L, Cn = x.shape
+    f32 = torch.float32
+    kept = (b, (L + SSD_GATED_SCAN_INTERVAL - 1) // SSD_GATED_SCAN_INTERVAL, Cn)
+    with _allocating_on(stream):
+        if y is None:
+            y = torch.empty_like(x)
+        if final_state is None and return_final_state:
+            final_state = torch.empty((b, Cn), dtype=f32, device=x.device)
+        if states is None and return_states:
+            states = torch.empty(kept, dtype=f32, device=x.device)
+    a = SsdGatedScanArgs(
+        batch=b, seqlen=L, channels=Cn, dtype=_dtype_code(x), scale=scale, x=_ptr(x),
+        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
+        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x), decay=_need(decay, "decay", (Cn,), f32, x),
+        reset=_reset_ptr(reset, (b, L), x), init_state=_opt(init_state, "init_state", (b, Cn), f32, x),
+        y=_need(y, "y", x.shape, x.dtype, x),
+        final_state=_opt(final_state, "final_state", (b, Cn), f32, x),
+        states=_opt(states, "states", kept, f32, x))
+    _run(lib.ssd_gated_scan, a, stream, x)
+    res = (y,) + tuple(t for t in (final_state, states) if t is not None)
+    return res if len(res) > 1 else y
+
+
+def ssd_gated_scan_bwd_workspace_size(batch, seqlen, channels, dtype=torch.bfloat16) -> int:
+    a = SsdGatedScanBwdArgs(batch=batch, seqlen=seqlen, channels=channels, scale=1.0,
+                            dtype=SSD_BF16 if dtype == torch.bfloat16 else SSD_F32)
+    return int(load_library().ssd_gated_scan_bwd_workspace_size(ctypes.byref(a)))
+
+
+def ssd_gated_scan_bwd(x, gate_a, gate_x, decay, dy, states, reset=None, d_final=None, *,
+                       scale: float = 8.0, out=None, workspace=None, stream=None) -> dict:
+    """Gradients of ssd_gated_scan: of sum(dy * y) + sum(d_final * final_state).
+    ``states`` is what the forward returned with return_states for the same
+    inputs.  Returns a dict dx, dgate_a, dgate_x (x's dtype), ddecay [C] and
+    d_init [b,C] (float32); ``out`` may hold preallocated tensors under the same
+    keys."""
+    lib = load_library()
+    b, L, Cn = x.shape
+    f32 = torch.float32
+    kept = (b, (L + SSD_GATED_SCAN_INTERVAL - 1) // SSD_GATED_SCAN_INTERVAL, Cn)
+    a = SsdGatedScanBwdArgs(
+        batch=b, seqlen=L, channels=Cn, dtype=_dtype_code(x), scale=scale, x=_ptr(x),
+        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
+        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x), decay=_need(decay, "decay", (Cn,), f32, x),
+        reset=_reset_ptr(reset, (b, L), x), states=_need(states, "states", kept, f32, x),
+        dy=_need(dy, "dy", x.shape, x.dtype, x), d_final=_opt(d_final, "d_final", (b, Cn), f32, x))
+    need = int(lib.ssd_gated_scan_bwd_workspace_size(ctypes.byref(a)))
+    if need == 0:
+        raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_gated_scan_bwd (sizes)")
+    o = dict(out or {})
+    shapes = (("dx", x.shape, x.dtype), ("dgate_a", x.shape, x.dtype), ("dgate_x", x.shape, x.dtype),
+              ("ddecay", (Cn,), f32), ("d_init", (b, Cn), f32))
+    with _allocating_on(stream):
+        for name, shape, dtype in shapes:
+            if name not in o:
+                o[name] = torch.empty(shape, dtype=dtype, device=x.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    for name, shape, dtype in shapes:
+        setattr(a, name, _need(o[name], name, shape, dtype, x))
+    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, x)
+    _run(lib.ssd_gated_scan_bwd, a, stream, x)
+    return o
+
+
+def ssd_gated_state_update(state, x, gate_a, gate_x, decay, reset=None, *, scale: float = 8.0,
+                           y=None, new_state=None, stream=None):
+    """One decode step of the gated linear recurrence: x, gate_a, gate_x [b,C] in
+    one dtype, decay [C] and state [b,C] float32, reset [b] bool or uint8.  The
+    state is updated in place unless ``new_state`` is given, which then receives
+    it.  Returns y [b,C]."""
+    lib = load_library()
+    b, Cn = x.shape
+    if y is None:
+        with _allocating_on(stream):
+            y = torch.empty_like(x)
+    sp = _need(state, "state", (b, Cn), torch.float32, x)
+    a = SsdGatedStateUpdateArgs(
+        batch=b, channels=Cn, dtype=_dtype_code(x), scale=scale, state=sp, x=_ptr(x),
+        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
+        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x),
+        decay=_need(decay, "decay", (Cn,), torch.float32, x), reset=_reset_ptr(reset, (b,), x),
+        new_state=sp if new_state is None else _need(new_state, "new_state", (b, Cn), torch.float32, x),
+        y=_need(y, "y", x.shape, x.dtype, x))
+    _run(lib.ssd_gated_state_update, a, stream, x)
+    return y
+
+
+def _head_rows(t, name, shape, like):
+    """(address, elements between tokens) of t [b,L,H,D], whose heads are dense
+    within a token and whose tokens are evenly spaced (a slice of packed rows)."""
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name} must be {like.dtype} on {like.device}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    b, L, H, D = t.shape
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 or (H > 1 and sh != D):
+        raise ValueError(f"{name}: the heads of a token must be dense")
+    if L > 1 and b > 1 and sb != L * sl:
+        raise ValueError(f"{name}: the tokens of all batch rows must be evenly spaced")
+    return t.data_ptr(), (sl if L > 1 else sb if b > 1 else H * D)
+
+
+def _qk_args(cls, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent):
+    b, L, hq, D = q.shape
+    f32 = torch.float32
+    a = cls(batch=b, seqlen=L, q_heads=hq, k_heads=0 if k is None else k.shape[2], headdim=D,
+            rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(), dtype=_dtype_code(q),
+            adjacent=1 if adjacent else 0, eps=eps, q_weight=_opt(q_weight, "q_weight", (D,), f32, q),
+            positions=_opt(positions, "positions", (b, L), torch.int64, q))
+    if inv_freq is not None:
+        a.inv_freq = _need(inv_freq, "inv_freq", (inv_freq.numel(),), f32, q)
+    a.q, a.q_stride = _head_rows(q, "q", None, q)
+    if k is not None:
+        a.k, a.k_stride = _head_rows(k, "k", (b, L, k.shape[2], D), q)
+        a.k_weight = _opt(k_weight, "k_weight", (D,), f32, q)
+    return a
+
+
+def ssd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, *, eps: float = 1e-5,
+                     adjacent: bool = False, q_out=None, k_out=None, stream=None):
+    """RMSNorm over each head of the queries and keys (C and B in the scan's dual
+    form) and, in the same pass, the rotation of each head's first
+    2 * len(inv_freq) elements by position * inv_freq: pairs (j, j + len) or,
+    with ``adjacent``, (2j, 2j + 1).  q [b,L,Hq,D], k [b,L,Hk,D] (or None) in one
+    dtype, each possibly a slice of packed rows (heads dense within a token,
+    tokens evenly spaced); q_weight, k_weight [D] float32 or None; inv_freq
+    float32 or None (no rotation); positions [b,L] int64 or None (0, 1, ... in
+    each row).  q_out / k_out may be q / k (in place) or such slices.  Returns
+    (q_out, k_out)."""
+    lib = load_library()
+    a = _qk_args(SsdQkNormRopeArgs, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent)
+    with _allocating_on(stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    a.q_out, a.q_out_stride = _head_rows(q_out, "q_out", q.shape, q)
+    if k is not None:
+        a.k_out, a.k_out_stride = _head_rows(k_out, "k_out", k.shape, q)
+    _run(lib.ssd_qk_norm_rope, a, stream, q)
+    return q_out, (k_out if k is not None else None)
+
+
+def ssd_qk_norm_rope_bwd_workspace_size(batch, seqlen, q_heads, k_heads, headdim, rot_dim,
+                                        dtype=torch.bfloat16) -> int:
+    a = SsdQkNormRopeBwdArgs(batch=batch, seqlen=seqlen, q_heads=q_heads, k_heads=k_heads,
+                             headdim=headdim, rot_dim=rot_dim,
+                             dtype=SSD_BF16 if dtype == torch.bfloat16 else SSD_F32)
+    return int(load_library().ssd_qk_norm_rope_bwd_workspace_size(ctypes.byref(a)))
+
+
+def ssd_qk_norm_rope_bwd(q, k, q_weight, k_weight, inv_freq, dq_out, dk_out, positions=None, *,
+                         eps: float = 1e-5, adjacent: bool = False, out=None, workspace=None,
+                         stream=None) -> dict:
+    """Gradients of ssd_qk_norm_rope from those of its outputs (dq_out, dk_out: q's
+    and k's shapes, dense or slices as there).  Returns a dict dq, dk (q's dtype;
+    dk absent without k), dq_weight, dk_weight [D] (float32); ``out`` may hold
+    preallocated tensors under the same keys, dq and dk also as slices of packed
+    rows."""
+    lib = load_library()
+    a = _qk_args(SsdQkNormRopeBwdArgs, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent)
+    need = int(lib.ssd_qk_norm_rope_bwd_workspace_size(ctypes.byref(a)))
+    if need == 0:
+        raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_qk_norm_rope_bwd (sizes)")
+    D = q.shape[3]
+    o = dict(out or {})
+    with _allocating_on(stream):
+        for name, t in (("q", q), ("k", k)):
+            if t is None:
+                continue
+            if "d" + name not in o:
+                o["d" + name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            if f"d{name}_weight" not in o:
+                o[f"d{name}_weight"] = torch.empty(D, dtype=torch.float32, device=t.device)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    a.dq_out, a.dq_out_stride = _head_rows(dq_out, "dq_out", q.shape, q)
+    a.dq, a.dq_stride = _head_rows(o["dq"], "dq", q.shape, q)
+    a.dq_weight = _need(o["dq_weight"], "dq_weight", (D,), torch.float32, q)
+    if k is not None:
+        a.dk_out, a.dk_out_stride = _head_rows(dk_out, "dk_out", k.shape, q)
+        a.dk, a.dk_stride = _head_rows(o["dk"], "dk", k.shape, q)
+        a.dk_weight = _need(o["dk_weight"], "dk_weight", (D,), torch.float32, q)
+    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, q)
+    _run(lib.ssd_qk_norm_rope_bwd, a, stream, q)
+    return o

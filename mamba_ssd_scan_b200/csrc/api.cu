@@ -7,6 +7,7 @@
 
 #include "gated_rmsnorm.h"
 #include "internal.cuh"
+#include "mixers.h"
 
 namespace {
 
@@ -14,6 +15,7 @@ using ssd::DecodeParams;
 using ssd::FwdParams;
 
 constexpr size_t kAlign = 256;
+constexpr int64_t kMaxTokens = 0x7fffffff;  // sequence lengths, channels, strides kept in 32 bits
 inline size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -270,6 +272,87 @@ SelWs sel_layout(const ssd_selective_scan_args& a) {
     w.sdt = round_up((size_t)a.batch * nc * a.channels * a.dstate * sizeof(float));
     w.total = w.sdt + round_up((size_t)a.batch * nc * a.channels * sizeof(float));
     return w;
+}
+
+// Sizes of the convolution's gradient.
+ssd_status check_conv_bwd_sizes(const ssd_conv1d_bwd_args* a) {
+    if (!a) return SSD_ERR_INVALID_ARG;
+    if (a->batch <= 0 || a->seqlen <= 0 || a->channels <= 0 || a->width <= 0)
+        return SSD_ERR_INVALID_ARG;
+    if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+    if (a->width > 8 || a->channels % (a->dtype == SSD_BF16 ? 8 : 4) != 0 || a->batch > 65535 ||
+        a->seqlen > kMaxTokens || a->channels > kMaxTokens)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Sizes of the gated linear recurrence (the decode step has seqlen 1).
+ssd_status check_gated_sizes(int64_t batch, int64_t seqlen, int64_t channels, int dtype, float scale) {
+    if (batch <= 0 || seqlen <= 0 || channels <= 0) return SSD_ERR_INVALID_ARG;
+    if (dtype != SSD_F32 && dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+    if (!(scale > 0.0f) || !(scale <= 3.4e38f)) return SSD_ERR_INVALID_ARG;
+    if (channels % (dtype == SSD_BF16 ? 8 : 4) != 0 || batch > 65535 || seqlen > kMaxTokens ||
+        channels > kMaxTokens)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Sizes of the head norm with the rotation, forward or backward.
+template <typename Args> ssd_status check_qk_sizes(const Args* a) {
+    if (!a) return SSD_ERR_INVALID_ARG;
+    if (a->batch <= 0 || a->seqlen <= 0 || a->q_heads <= 0 || a->k_heads < 0 || a->headdim <= 0 ||
+        a->rot_dim < 0 || a->rot_dim > a->headdim)
+        return SSD_ERR_INVALID_ARG;
+    if (a->dtype != SSD_F32 && a->dtype != SSD_BF16) return SSD_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.0f) || !(a->eps <= 3.4e38f)) return SSD_ERR_INVALID_ARG;
+    if (a->headdim % 8 != 0 || a->headdim > 256 || a->rot_dim % 16 != 0 || a->q_heads > 65536 ||
+        a->k_heads > 65536 || a->q_heads + a->k_heads > 65536 || a->seqlen > kMaxTokens ||
+        a->batch > kMaxTokens / a->seqlen)
+        return SSD_ERR_UNSUPPORTED;
+    return SSD_OK;
+}
+
+// Token strides {q, q', k, k'}: at least the dense heads, whole 16-byte vectors.
+ssd_status check_qk_strides(const int64_t* s, int64_t q_heads, int64_t k_heads, int64_t headdim, int dtype) {
+    for (int i = 0; i < 4; ++i) {
+        const int64_t heads = i < 2 ? q_heads : k_heads;
+        if (heads == 0) continue;
+        if (s[i] < heads * headdim) return SSD_ERR_INVALID_ARG;
+        if (s[i] % (dtype == SSD_BF16 ? 8 : 4) != 0 || s[i] > kMaxTokens) return SSD_ERR_UNSUPPORTED;
+    }
+    return SSD_OK;
+}
+
+template <typename Args> bool check_qk_inputs(const Args* a) {
+    return check_ptr(a->q, false, true) && check_ptr(a->k, a->k_heads == 0, true) &&
+           check_ptr(a->q_weight, true, true) && check_ptr(a->k_weight, true, true) &&
+           check_ptr(a->inv_freq, a->rot_dim == 0, true) &&
+           (reinterpret_cast<uintptr_t>(a->positions) & 7u) == 0 && check_ptr(a->positions, true, false);
+}
+
+template <typename Args> ssd::NormRopeParams qk_params(const Args* a) {
+    ssd::NormRopeParams p{};
+    p.batch = a->batch;
+    p.seqlen = a->seqlen;
+    p.heads[0] = static_cast<int>(a->q_heads);
+    p.heads[1] = static_cast<int>(a->k_heads);
+    p.headdim = static_cast<int>(a->headdim);
+    p.rot_dim = static_cast<int>(a->rot_dim);
+    p.adjacent = a->adjacent ? 1 : 0;
+    p.eps = a->eps;
+    p.in[0] = a->q;
+    p.in[1] = a->k;
+    p.in_stride[0] = a->q_stride;
+    p.in_stride[1] = a->k_stride;
+    p.weight[0] = a->q_weight;
+    p.weight[1] = a->k_weight;
+    p.inv_freq = a->inv_freq;
+    p.positions = a->positions;
+    return p;
+}
+
+size_t qk_partial_bytes(const ssd_qk_norm_rope_bwd_args& a) {
+    return round_up(static_cast<size_t>(ssd::norm_rope_bwd_rows()) * a.headdim * sizeof(float));
 }
 
 // Largest opt-in shared memory per CTA on sm_100 (227 KB).
@@ -687,6 +770,199 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* a, void* stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return to_status(a->dtype == SSD_BF16 ? ssd::launch_conv1d<__nv_bfloat16>(p, true, s)
                                           : ssd::launch_conv1d<float>(p, true, s));
+}
+
+size_t ssd_causal_conv1d_bwd_workspace_size(const ssd_conv1d_bwd_args* a) {
+    if (check_conv_bwd_sizes(a) != SSD_OK) return 0;
+    return round_up(ssd::conv1d_bwd_partial_bytes(a->batch, a->seqlen, a->channels, a->width));
+}
+
+ssd_status ssd_causal_conv1d_bwd(const ssd_conv1d_bwd_args* a, void* stream) {
+    const ssd_status st = check_conv_bwd_sizes(a);
+    if (st != SSD_OK) return st;
+    if (!check_ptr(a->x, false, true) || !check_ptr(a->weight, false, false) ||
+        !check_ptr(a->bias, true, false) || !check_ptr(a->init_state, true, false) ||
+        !check_ptr(a->dy, false, true) || !check_ptr(a->d_final, true, false) ||
+        !check_ptr(a->dx, false, true) || !check_ptr(a->dweight, false, false) ||
+        !check_ptr(a->dbias, true, false) || !check_ptr(a->d_init, true, false))
+        return SSD_ERR_INVALID_ARG;
+    if (a->workspace_bytes < ssd_causal_conv1d_bwd_workspace_size(a) ||
+        !check_ptr(a->workspace, false, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::ConvBwdParams p;
+    p.batch = a->batch;
+    p.seqlen = a->seqlen;
+    p.channels = a->channels;
+    p.width = a->width;
+    p.activation = a->activation ? 1 : 0;
+    p.x = a->x;
+    p.weight = a->weight;
+    p.bias = a->bias;
+    p.init_state = a->init_state;
+    p.dy = a->dy;
+    p.d_final = a->d_final;
+    p.dx = a->dx;
+    p.dweight = a->dweight;
+    p.dbias = a->dbias;
+    p.d_init = a->d_init;
+    p.partial = static_cast<float*>(a->workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_conv1d_bwd<__nv_bfloat16>(p, s)
+                                          : ssd::launch_conv1d_bwd<float>(p, s));
+}
+
+ssd_status ssd_gated_scan(const ssd_gated_scan_args* a, void* stream) {
+    if (!a) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = check_gated_sizes(a->batch, a->seqlen, a->channels, a->dtype, a->scale);
+    if (st != SSD_OK) return st;
+    if (!check_ptr(a->x, false, true) || !check_ptr(a->gate_a, false, true) ||
+        !check_ptr(a->gate_x, false, true) || !check_ptr(a->decay, false, true) ||
+        !check_ptr(a->reset, true, false) || !check_ptr(a->init_state, true, true) ||
+        !check_ptr(a->y, false, true) || !check_ptr(a->final_state, true, true) ||
+        !check_ptr(a->states, true, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::GatedScanParams p{};
+    p.batch = a->batch;
+    p.seqlen = a->seqlen;
+    p.channels = a->channels;
+    p.scale = a->scale;
+    p.x = a->x;
+    p.gate_a = a->gate_a;
+    p.gate_x = a->gate_x;
+    p.decay = a->decay;
+    p.reset = a->reset;
+    p.init_state = a->init_state;
+    p.y = a->y;
+    p.final_state = a->final_state;
+    p.states = a->states;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_gated_scan<__nv_bfloat16>(p, s)
+                                          : ssd::launch_gated_scan<float>(p, s));
+}
+
+size_t ssd_gated_scan_bwd_workspace_size(const ssd_gated_scan_bwd_args* a) {
+    if (!a || check_gated_sizes(a->batch, a->seqlen, a->channels, a->dtype, a->scale) != SSD_OK) return 0;
+    return round_up(ssd::gated_scan_bwd_partial_bytes(a->batch, a->seqlen, a->channels));
+}
+
+ssd_status ssd_gated_scan_bwd(const ssd_gated_scan_bwd_args* a, void* stream) {
+    if (!a) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = check_gated_sizes(a->batch, a->seqlen, a->channels, a->dtype, a->scale);
+    if (st != SSD_OK) return st;
+    if (!check_ptr(a->x, false, true) || !check_ptr(a->gate_a, false, true) ||
+        !check_ptr(a->gate_x, false, true) || !check_ptr(a->decay, false, true) ||
+        !check_ptr(a->reset, true, false) || !check_ptr(a->states, false, true) ||
+        !check_ptr(a->dy, false, true) || !check_ptr(a->d_final, true, true) ||
+        !check_ptr(a->dx, false, true) || !check_ptr(a->dgate_a, false, true) ||
+        !check_ptr(a->dgate_x, false, true) || !check_ptr(a->ddecay, false, true) ||
+        !check_ptr(a->d_init, true, true))
+        return SSD_ERR_INVALID_ARG;
+    if (a->workspace_bytes < ssd_gated_scan_bwd_workspace_size(a) || !check_ptr(a->workspace, false, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::GatedScanParams p{};
+    p.batch = a->batch;
+    p.seqlen = a->seqlen;
+    p.channels = a->channels;
+    p.scale = a->scale;
+    p.x = a->x;
+    p.gate_a = a->gate_a;
+    p.gate_x = a->gate_x;
+    p.decay = a->decay;
+    p.reset = a->reset;
+    p.states = const_cast<float*>(a->states);
+    p.dy = a->dy;
+    p.d_final = a->d_final;
+    p.dx = a->dx;
+    p.dgate_a = a->dgate_a;
+    p.dgate_x = a->dgate_x;
+    p.ddecay = a->ddecay;
+    p.d_init = a->d_init;
+    p.partial = static_cast<float*>(a->workspace);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_gated_scan_bwd<__nv_bfloat16>(p, s)
+                                          : ssd::launch_gated_scan_bwd<float>(p, s));
+}
+
+ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* a, void* stream) {
+    if (!a) return SSD_ERR_INVALID_ARG;
+    const ssd_status st = check_gated_sizes(a->batch, 1, a->channels, a->dtype, a->scale);
+    if (st != SSD_OK) return st;
+    if (!check_ptr(a->state, false, true) || !check_ptr(a->x, false, true) ||
+        !check_ptr(a->gate_a, false, true) || !check_ptr(a->gate_x, false, true) ||
+        !check_ptr(a->decay, false, true) || !check_ptr(a->reset, true, false) ||
+        !check_ptr(a->new_state, false, true) || !check_ptr(a->y, false, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::GatedUpdateParams p;
+    p.batch = a->batch;
+    p.channels = a->channels;
+    p.scale = a->scale;
+    p.state = a->state;
+    p.x = a->x;
+    p.gate_a = a->gate_a;
+    p.gate_x = a->gate_x;
+    p.decay = a->decay;
+    p.reset = a->reset;
+    p.new_state = a->new_state;
+    p.y = a->y;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_gated_update<__nv_bfloat16>(p, s)
+                                          : ssd::launch_gated_update<float>(p, s));
+}
+
+ssd_status ssd_qk_norm_rope(const ssd_qk_norm_rope_args* a, void* stream) {
+    ssd_status st = check_qk_sizes(a);
+    if (st != SSD_OK) return st;
+    const int64_t strides[4] = {a->q_stride, a->q_out_stride, a->k_stride, a->k_out_stride};
+    if ((st = check_qk_strides(strides, a->q_heads, a->k_heads, a->headdim, a->dtype)) != SSD_OK) return st;
+    if (!check_qk_inputs(a) || !check_ptr(a->q_out, false, true) ||
+        !check_ptr(a->k_out, a->k_heads == 0, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::NormRopeParams p = qk_params(a);
+    p.out[0] = a->q_out;
+    p.out[1] = a->k_out;
+    p.out_stride[0] = a->q_out_stride;
+    p.out_stride[1] = a->k_out_stride;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_norm_rope<__nv_bfloat16>(p, s)
+                                          : ssd::launch_norm_rope<float>(p, s));
+}
+
+size_t ssd_qk_norm_rope_bwd_workspace_size(const ssd_qk_norm_rope_bwd_args* a) {
+    if (check_qk_sizes(a) != SSD_OK) return 0;
+    return 2 * qk_partial_bytes(*a);
+}
+
+ssd_status ssd_qk_norm_rope_bwd(const ssd_qk_norm_rope_bwd_args* a, void* stream) {
+    ssd_status st = check_qk_sizes(a);
+    if (st != SSD_OK) return st;
+    const int64_t sin[4] = {a->q_stride, a->dq_out_stride, a->k_stride, a->dk_out_stride};
+    const int64_t sout[4] = {a->dq_stride, a->dq_stride, a->dk_stride, a->dk_stride};
+    if ((st = check_qk_strides(sin, a->q_heads, a->k_heads, a->headdim, a->dtype)) != SSD_OK) return st;
+    if ((st = check_qk_strides(sout, a->q_heads, a->k_heads, a->headdim, a->dtype)) != SSD_OK) return st;
+    const bool no_k = a->k_heads == 0;
+    if (!check_qk_inputs(a) || !check_ptr(a->dq_out, false, true) || !check_ptr(a->dk_out, no_k, true) ||
+        !check_ptr(a->dq, false, true) || !check_ptr(a->dk, no_k, true) ||
+        !check_ptr(a->dq_weight, true, false) || !check_ptr(a->dk_weight, true, false))
+        return SSD_ERR_INVALID_ARG;
+    if (a->workspace_bytes < ssd_qk_norm_rope_bwd_workspace_size(a) || !check_ptr(a->workspace, false, true))
+        return SSD_ERR_INVALID_ARG;
+    ssd::NormRopeParams p = qk_params(a);
+    p.dout[0] = a->dq_out;
+    p.dout[1] = a->dk_out;
+    p.dout_stride[0] = a->dq_out_stride;
+    p.dout_stride[1] = a->dk_out_stride;
+    p.din[0] = a->dq;
+    p.din[1] = a->dk;
+    p.din_stride[0] = a->dq_stride;
+    p.din_stride[1] = a->dk_stride;
+    p.dweight[0] = a->dq_weight;
+    p.dweight[1] = no_k ? nullptr : a->dk_weight;
+    char* ws = static_cast<char*>(a->workspace);
+    p.partial[0] = reinterpret_cast<float*>(ws);
+    p.partial[1] = reinterpret_cast<float*>(ws + qk_partial_bytes(*a));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return to_status(a->dtype == SSD_BF16 ? ssd::launch_norm_rope_bwd<__nv_bfloat16>(p, s)
+                                          : ssd::launch_norm_rope_bwd<float>(p, s));
 }
 
 ssd_status ssd_gated_rmsnorm(const ssd_gated_rmsnorm_args* a, void* stream) {
