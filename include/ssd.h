@@ -537,6 +537,11 @@ typedef struct {
 
 ssd_status ssd_gated_scan(const ssd_gated_scan_args* args, void* stream);
 
+/* Synchronises `stream` and returns SSD_ERR_TIMEOUT if a ssd_gated_scan or
+ * ssd_gated_scan_bwd launch on this device gave up on an internal wait since
+ * the last check (its outputs are invalid; the flag is cleared), else SSD_OK. */
+ssd_status ssd_gated_scan_check_status(void* stream);
+
 /* Gradients of ssd_gated_scan: of J = sum dy . y + d_final . h_L with respect to
  * x, gate_a, gate_x, decay and init_state.  `states` is the forward's (same
  * inputs); h is recomputed from it inside each 64-token interval.  With the
@@ -721,12 +726,16 @@ const char* ssd_version(void);
  * 128-token tiles one cluster of CTAs takes; the next run's wait gives up
  * after about a second; SSD_FLAG_SINGLE_PASS only); SSD_DEBUG_SCAN_DECAYS: the
  * tensor-core chunk_scan does not hand the decays of the first head of chunk
- * `index` to its workers, whose waits give up.  index < 0 turns the hook off.
+ * `index` to its workers, whose waits give up; SSD_DEBUG_GATED_MAP: the first
+ * tile of a cluster does not send its map in round `index` of the gated
+ * recurrence (calls whose sequence is spread over several CTAs).  index < 0
+ * turns the hook off.
  * Process-wide; read on the host when a kernel is launched.  Other values of
  * `what` are ignored. */
 #define SSD_DEBUG_CONV_TILE 0
 #define SSD_DEBUG_FWD_CARRY 1
 #define SSD_DEBUG_SCAN_DECAYS 2
+#define SSD_DEBUG_GATED_MAP 3
 void ssd_debug_set_withhold(int what, int64_t index);
 
 #ifdef __cplusplus

@@ -18,7 +18,7 @@ import torch
 __all__ = [
     "SsdError", "ssd_fwd", "ssd_fwd_workspace_size", "ssd_fwd_check_status", "ssd_fwd_no_alloc",
     "ssd_fwd_no_alloc_check_status", "ssd_fwd_no_alloc_scratch_bytes", "ssd_debug_set_withhold",
-    "SSD_DEBUG_CONV_TILE", "SSD_DEBUG_FWD_CARRY", "SSD_DEBUG_SCAN_DECAYS",
+    "SSD_DEBUG_CONV_TILE", "SSD_DEBUG_FWD_CARRY", "SSD_DEBUG_SCAN_DECAYS", "SSD_DEBUG_GATED_MAP",
     "ssd_fwd_tensor_core_steps", "tensor_core_steps", "ssd_chunk_cumsum", "ssd_chunk_state",
     "ssd_state_passing", "ssd_chunk_scan", "ssd_state_passing_hilo", "ssd_chunk_scan_hilo",
     "ssd_state_update", "ssd_status_string",
@@ -31,6 +31,7 @@ __all__ = [
     "ssd_selective_state_update", "ssd_gated_rmsnorm",
     "ssd_causal_conv1d_bwd", "ssd_causal_conv1d_bwd_workspace_size",
     "ssd_gated_scan", "ssd_gated_scan_bwd", "ssd_gated_scan_bwd_workspace_size",
+    "ssd_gated_scan_check_status",
     "ssd_gated_state_update", "SSD_GATED_SCAN_INTERVAL",
     "ssd_qk_norm_rope", "ssd_qk_norm_rope_bwd", "ssd_qk_norm_rope_bwd_workspace_size",
 ]
@@ -264,6 +265,8 @@ def load_library():
     lib.ssd_qk_norm_rope_bwd.argtypes = [ctypes.POINTER(SsdQkNormRopeBwdArgs), _vp]
     lib.ssd_qk_norm_rope_bwd_workspace_size.restype = _sz
     lib.ssd_qk_norm_rope_bwd_workspace_size.argtypes = [ctypes.POINTER(SsdQkNormRopeBwdArgs)]
+    lib.ssd_gated_scan_check_status.restype = ctypes.c_int
+    lib.ssd_gated_scan_check_status.argtypes = [_vp]
     lib.ssd_conv1d_check_status.restype = ctypes.c_int
     lib.ssd_conv1d_check_status.argtypes = [_vp]
     lib.ssd_status_string.restype = ctypes.c_char_p
@@ -461,6 +464,7 @@ def ssd_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, chunk: int = 256, init_sta
 SSD_DEBUG_CONV_TILE = 0
 SSD_DEBUG_FWD_CARRY = 1
 SSD_DEBUG_SCAN_DECAYS = 2
+SSD_DEBUG_GATED_MAP = 3
 
 
 def ssd_debug_set_withhold(what: int, index: int) -> None:
@@ -908,6 +912,13 @@ def ssd_gated_scan(x, gate_a, gate_x, decay, init_state=None, reset=None, *, sca
     _run(lib.ssd_gated_scan, a, stream, x)
     res = (y,) + tuple(t for t in (final_state, states) if t is not None)
     return res if len(res) > 1 else y
+
+
+def ssd_gated_scan_check_status(stream=None) -> int:
+    """Synchronises the stream; SSD_ERR_TIMEOUT if a ssd_gated_scan or
+    ssd_gated_scan_bwd on this device gave up on an internal wait since the last
+    check, else 0."""
+    return int(load_library().ssd_gated_scan_check_status(_stream_ptr(stream)))
 
 
 def ssd_gated_scan_bwd_workspace_size(batch, seqlen, channels, dtype=torch.bfloat16) -> int:

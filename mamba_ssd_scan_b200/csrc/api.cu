@@ -374,12 +374,12 @@ ssd_status check_bwd_sizes(const ssd_bwd_args* a) {
 }  // namespace
 
 namespace {
-std::atomic<int64_t> g_withhold[3] = {{-1}, {-1}, {-1}};
+std::atomic<int64_t> g_withhold[4] = {{-1}, {-1}, {-1}, {-1}};
 }  // namespace
 
 namespace ssd {
 int64_t debug_withhold(int what) {
-    return (what >= 0 && what < 3) ? g_withhold[what].load(std::memory_order_relaxed) : -1;
+    return (what >= 0 && what < 4) ? g_withhold[what].load(std::memory_order_relaxed) : -1;
 }
 }  // namespace ssd
 
@@ -840,6 +840,13 @@ ssd_status ssd_gated_scan(const ssd_gated_scan_args* a, void* stream) {
                                           : ssd::launch_gated_scan<float>(p, s));
 }
 
+ssd_status ssd_gated_scan_check_status(void* stream) {
+    int v = 0;
+    if (ssd::gated_scan_take_status(&v, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return SSD_ERR_CUDA;
+    return v == 0 ? SSD_OK : static_cast<ssd_status>(v);
+}
+
 size_t ssd_gated_scan_bwd_workspace_size(const ssd_gated_scan_bwd_args* a) {
     if (!a || check_gated_sizes(a->batch, a->seqlen, a->channels, a->dtype, a->scale) != SSD_OK) return 0;
     return round_up(ssd::gated_scan_bwd_partial_bytes(a->batch, a->seqlen, a->channels));
@@ -1042,7 +1049,7 @@ const char* ssd_last_cuda_error(void) {
 }
 
 void ssd_debug_set_withhold(int what, int64_t index) {
-    if (what >= 0 && what < 3) g_withhold[what].store(index < 0 ? -1 : index, std::memory_order_relaxed);
+    if (what >= 0 && what < 4) g_withhold[what].store(index < 0 ? -1 : index, std::memory_order_relaxed);
 }
 
 const char* ssd_version(void) { return "ssd_b200 0.1.0 (sm_100a)"; }

@@ -2,29 +2,37 @@
 // step (the formulas stand in include/ssd.h).
 //
 // A step h <- a h + u is an affine map, and maps compose: (A, H) after (A', H')
-// is (A A', A H' + H).  So a sequence is cut into groups of consecutive
+// is (A A', A H' + H).  So a sequence is cut into groups of 8 consecutive
 // tokens, each thread runs its group from zero, the groups' maps are composed,
 // and each thread then replays its group from the state that enters it.  The
 // replay costs two packed operations per token on values that are still in
 // registers, while the gates (about 4 special-function results per element)
 // are formed once and the inputs are read once.
 //
-// A warp takes one group of tokens of 64 channels (a pair per lane); the 8
-// warps of a CTA take consecutive groups, and the CTAs of a cluster consecutive
-// tiles, whose maps they exchange through distributed shared memory, one
-// cluster barrier per round of cluster x tile tokens.  Then every CTA knows the
-// state entering its tile and the one entering the next round.  The order of
-// composition is fixed, so results do not depend on timing, and there is no
-// workspace and no wait on another cluster.
+// A compute warp takes one group of tokens of 64 channels (a pair per lane);
+// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens),
+// and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
+// tile's map, sends it to the cluster's CTAs through distributed shared memory
+// (asynchronous stores that complete on the receiver's mbarrier), and hands
+// each group its entering state.  The order of composition is fixed, so
+// results do not depend on timing; there is no workspace and no wait on another
+// cluster.  Every mbarrier wait is bounded: on expiry the CTA raises its abort
+// flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
+#include <stdlib.h>
 #include "mixers.h"
+#include "tcgen05.cuh"
+#include "tma.cuh"
 #include "vec16.cuh"
 
 namespace ssd {
 namespace {
 
 constexpr int kInterval = SSD_GATED_SCAN_INTERVAL;
-constexpr int NW = 8;            // warps (groups) per CTA
-constexpr int TPB = NW * 32;
+constexpr int NW = 8;            // compute warps (groups) per CTA
+constexpr int TPB = (NW + 1) * 32;
+constexpr int TPT = 8;           // tokens per group
+constexpr int TILE = NW * TPT;   // tokens per CTA and round
+static_assert(TILE == kInterval, "a tile starts where a state is kept");
 constexpr int CPB = 64;          // channels per CTA
 constexpr int kMaxCluster = 16;
 
@@ -64,13 +72,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // inputs the rounding of k v (up to 2^-24 |k v| in the exponent) is carried
 // along; for bf16 inputs it stays well inside their own 2^-9.
 template <bool EXACT>
-__device__ __forceinline__ float exp2_scaled(float v, float hi, float lo, float top = 126.0f) {
-    if constexpr (EXACT) v = min_nan(max_nan(v, -200.0f), 200.0f);  // no infinite products below
-    const float t = min_nan(v * hi, top);
-    float e = ex2_approx(t);
+__device__ __forceinline__ float2 exp2_scaled(float2 v, float hi, float lo, float top = 126.0f) {
+    if constexpr (EXACT)  // no infinite products below
+        v = make_float2(min_nan(max_nan(v.x, -200.0f), 200.0f), min_nan(max_nan(v.y, -200.0f), 200.0f));
+    const float2 t = mul2(v, dup(hi));
+    float2 e = make_float2(ex2_approx(min_nan(t.x, top)), ex2_approx(min_nan(t.y, top)));
     if constexpr (EXACT) {
-        const float d = fmaf(v, lo, fmaf(v, hi, -(v * hi)));  // what t lost
-        e = fmaf(e, d * 0.69314718f, e);
+        const float2 d = fma2(v, dup(lo), fma2(v, dup(hi), make_float2(-t.x, -t.y)));  // what t lost
+        e = fma2(e, mul2(d, dup(0.69314718f)), e);
     }
     return e;
 }
@@ -86,10 +95,8 @@ constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.925962991126
 template <bool EXACT>
 __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& i) {
     const float2 one = dup(1.0f);
-    const float2 ea = add2(make_float2(exp2_scaled<EXACT>(ga.x, -kLog2eHi, -kLog2eLo),
-                                       exp2_scaled<EXACT>(ga.y, -kLog2eHi, -kLog2eLo)), one);
-    const float2 ex = add2(make_float2(exp2_scaled<EXACT>(gx.x, -kLog2eHi, -kLog2eLo, 60.0f),
-                                       exp2_scaled<EXACT>(gx.y, -kLog2eHi, -kLog2eLo, 60.0f)), one);
+    const float2 ea = add2(exp2_scaled<EXACT>(ga, -kLog2eHi, -kLog2eLo), one);
+    const float2 ex = add2(exp2_scaled<EXACT>(gx, -kLog2eHi, -kLog2eLo, 60.0f), one);
     const float2 d = mul2(ea, ex);
     const float2 inv = make_float2(rcp_approx(d.x), rcp_approx(d.y));
     r = mul2(inv, ex);
@@ -98,32 +105,35 @@ __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& 
 
 // em1 = a - 1 = e^la - 1 (la <= 0) and a.  a = 1 + em1 enters the recurrence as
 // h + em1 h, so that a decay near 1 keeps its relative accuracy in la, and
-// 1 - a^2 = -em1 (2 + em1) without cancellation.  Below -1/4 from e^la, above
-// from the Taylor series to the seventh power (cut off at 2^-24 of em1); the usual decays
-// (a slowest one of 0.9 to 0.999 per channel) take the series only, which
-// saves them a special-function result.
+// 1 - a^2 = -em1 (2 + em1) without cancellation.  Down to -1/4 from the Taylor
+// series to the sixth power (what it leaves out is below 2^-24 of em1), beyond
+// from e^la.  la never falls below the channel's own -scale softplus(decay),
+// so where that is above -1/4 (`slow`, the same for a whole warp; the usual
+// decays of 0.9 to 0.999 at the open gate) the second form is not evaluated.
 template <bool EXACT>
-__device__ __forceinline__ void decays(float2 la, float2& em1, float2& a) {
-    float2 q = dup(1.0f / 5040.0f);
-    q = fma2(q, la, dup(1.0f / 720.0f));
+__device__ __forceinline__ void decays(float2 la, bool slow, float2& em1, float2& a) {
+    float2 q = dup(1.0f / 720.0f);
     q = fma2(q, la, dup(1.0f / 120.0f));
     q = fma2(q, la, dup(1.0f / 24.0f));
     q = fma2(q, la, dup(1.0f / 6.0f));
     q = fma2(q, la, dup(0.5f));
     em1 = fma2(mul2(q, la), la, la);
     a = add2(em1, dup(1.0f));
-    if (la.x < -0.25f) {
-        a.x = exp2_scaled<EXACT>(la.x, kLog2eHi, kLog2eLo);
-        em1.x = a.x - 1.0f;
-    }
-    if (la.y < -0.25f) {
-        a.y = exp2_scaled<EXACT>(la.y, kLog2eHi, kLog2eLo);
-        em1.y = a.y - 1.0f;
+    if (!slow) {
+        const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
+        if (!(la.x >= -0.25f)) {
+            a.x = e.x;
+            em1.x = e.x - 1.0f;
+        }
+        if (!(la.y >= -0.25f)) {
+            a.y = e.y;
+            em1.y = e.y - 1.0f;
+        }
     }
 }
 // sqrt(1 - a^2)
 __device__ __forceinline__ float2 input_weight(float2 em1) {
-    const float2 n2 = mul2(make_float2(-em1.x, -em1.y), add2(em1, dup(2.0f)));
+    const float2 n2 = mul2(em1, fma2(em1, dup(-1.0f), dup(-2.0f)));
     return make_float2(sqrt_approx(n2.x), sqrt_approx(n2.y));
 }
 // -scale * softplus(decay) of a pair of channels (0 outside them)
@@ -134,45 +144,68 @@ __device__ __forceinline__ float2 decay_rates(const GatedScanParams& p, int64_t 
 __device__ __forceinline__ float sigma_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // ---- clusters ----
-__device__ __forceinline__ void cluster_arrive() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+// the shared::cluster address of this CTA's shared variable in CTA `rank`
+__device__ __forceinline__ uint32_t in_rank(const void* mine, int rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(tc::smem_u32(mine)), "r"(rank));
+    return r;
 }
-// a float4 into the same shared variable of the cluster's CTA `rank`
-__device__ __forceinline__ void store_remote(const float4* mine, int rank, float4 v) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};"
+// asynchronous stores into a CTA of the cluster that complete on its mbarrier
+__device__ __forceinline__ void store_async(uint32_t dst, float4 v, uint32_t mbar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];"
                  :
-                 : "r"(r), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "r"(dst), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(mbar)
                  : "memory");
 }
-__device__ __forceinline__ void store_remote(const int* mine, int rank, int v) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(mine)), r;
-    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.s32 [%0], %1;" : : "r"(r), "r"(v) : "memory");
+__device__ __forceinline__ void store_async(uint32_t dst, int v, uint32_t mbar) {
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.s32 [%0], %1, [%2];"
+                 :
+                 : "r"(dst), "r"(v), "r"(mbar)
+                 : "memory");
 }
+// bounded wait on a local mbarrier that peers complete; false once aborted
+__device__ __forceinline__ bool wait_cluster(uint32_t mbar, uint32_t parity, volatile int* abort) {
+    for (uint32_t i = 0; i < tc::kSpinLimit; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=r"(ok)
+            : "r"(mbar), "r"(parity), "r"(200)
+            : "memory");
+        if (ok) return true;
+        if ((i & 63) == 63 && *abort) return false;
+    }
+    *abort = 1;
+    return false;
+}
+
+// SSD_ERR_TIMEOUT once a scan or its gradient gave up on a wait; read and
+// cleared by ssd_gated_scan_check_status.
+__device__ int g_gated_status;
 
 // ---- a warp's tile of one array: TPT rows of 64 channels, by 16-byte copies ----
 template <typename T, int TPT> struct Tile {
     static constexpr int kRowBytes = CPB * sizeof(T);
     static constexpr int kBytes = TPT * kRowBytes;
-    // rows t0 .. t0 + TPT - 1 of src [L][C], from channel c0; zeros past L and C
-    static __device__ __forceinline__ void load(uint8_t* dst, const T* src, int64_t t0, int64_t L, int64_t c0,
-                                                int64_t C, int lane) {
-        constexpr int CH = kRowBytes / 16;  // chunks per row
+    static constexpr int kChunks = kRowBytes / 16;          // per row
+    static constexpr int kRows = 32 / kChunks;              // rows per copy instruction
+    static constexpr int kElems = 16 / static_cast<int>(sizeof(T));
+    // rows 0 .. TPT - 1 of the array whose row 0 the lane's own chunk starts at src (row
+    // stride C elements); rows from `left` on and, without `in`, all of the lane's chunks read as zero
+    static __device__ __forceinline__ void load(uint8_t* dst, const T* src, int left, bool in, int64_t C, int lane) {
+        uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + lane * 16;
+        const int n = in ? left - lane / kChunks : 0;  // rows of this lane's column of chunks
 #pragma unroll
-        for (int k = 0; k < TPT * CH / 32; ++k) {
-            const int row = (lane + 32 * k) / CH, ch = (lane + 32 * k) % CH;
-            const int64_t c = c0 + ch * (16 / static_cast<int>(sizeof(T)));
-            const bool in = t0 + row < L && c < C;
-            const T* g = in ? src + (t0 + row) * C + c : src;
-            const uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst + row * kRowBytes + ch * 16));
+        for (int k = 0; k < TPT / kRows; ++k) {
+            const bool on = k * kRows < n;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                          :
-                         : "r"(s), "l"(g), "r"(in ? 16 : 0)
+                         : "r"(s + k * 512), "l"(on ? src + k * kRows * C : nullptr), "r"(on ? 16 : 0)
                          : "memory");
         }
     }
@@ -200,133 +233,181 @@ __device__ __forceinline__ float2 apply(float4 m, bool restart, float2 h) {
     return restart ? H : fma2(make_float2(m.x, m.y), h, H);
 }
 
-template <typename T> constexpr int kFwdTokens = sizeof(T) == 2 ? 16 : 8;  // tokens per thread
+struct Exchange {
+    float4 group_map[NW][32];             // this CTA's groups
+    float4 tile_map[2][kMaxCluster][32];  // the cluster's tiles, two rounds
+    float2 entering[NW][32];              // the state entering each group
+    int group_rst[NW], tile_rst[2][kMaxCluster];
+    uint64_t maps_ready, states_ready, tiles_ready[2];
+    int abort;
+};
+
+// 16-byte copies in flight ahead of the arithmetic, in groups of tokens
+constexpr int kStages = 2;
 
 template <typename T, bool RESET>
-__global__ void __launch_bounds__(TPB, 2) gated_scan_kernel(GatedScanParams p, int cl) {
-    constexpr int TPT = kFwdTokens<T>;
-    constexpr int TILE = NW * TPT;
+__global__ void __launch_bounds__(TPB, 3) gated_scan_kernel(GatedScanParams p, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
     using TL = Tile<T, TPT>;
-    extern __shared__ __align__(16) uint8_t ring[];    // [NW][3] tiles
-    __shared__ float4 group_map[2][NW][32];             // this CTA's groups
-    __shared__ float4 tile_map[2][kMaxCluster][32];     // the cluster's tiles
-    __shared__ int group_rst[2][NW], tile_rst[2][kMaxCluster];
+    extern __shared__ __align__(16) uint8_t ring[];    // [NW][kStages][3] tiles
+    __shared__ Exchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
     const int rank = static_cast<int>(blockIdx.x) % cl;
     const int64_t c0 = static_cast<int64_t>(blockIdx.x / cl) * CPB, c = c0 + 2 * lane;
     const bool active = c < C;
-    const T* x = static_cast<const T*>(p.x) + b * L * C;
-    const T* ga = static_cast<const T*>(p.gate_a) + b * L * C;
-    const T* gx = static_cast<const T*>(p.gate_x) + b * L * C;
-    T* y = static_cast<T*>(p.y) + b * L * C + c;
-    const int64_t nst = (L + kInterval - 1) / kInterval;
-    uint8_t* tiles = ring + warp * 3 * TL::kBytes;
-    auto fetch = [&](int64_t t0) {
-        TL::load(tiles, x, t0, L, c0, C, lane);
-        TL::load(tiles + TL::kBytes, ga, t0, L, c0, C, lane);
-        TL::load(tiles + 2 * TL::kBytes, gx, t0, L, c0, C, lane);
-        copies_commit();
-    };
     const int64_t round = static_cast<int64_t>(cl) * TILE;
-    int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;
-    fetch(t0);
-    const float2 k = decay_rates(p, c, active);
-    float2 carry = (active && p.init_state) ? *reinterpret_cast<const float2*>(p.init_state + b * C + c)
-                                            : dup(0.0f);
-    if (cl > 1) {  // every CTA of the cluster runs before its shared memory is written
-        cluster_arrive();
-        cluster_wait();
+    const int rounds = static_cast<int>((L + round - 1) / round);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(tc::smem_u32(&ex.maps_ready), NW);
+        tc::mbar_init(tc::smem_u32(&ex.states_ready), 1);
+        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[0]), 1);
+        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[1]), 1);
+        tc::fence_mbar_init();
+        ex.abort = 0;
     }
-    int buf = 0;
-    for (int64_t tr = 0; tr < L; tr += round, t0 += round, buf ^= 1) {
-        uint32_t rst = 0;
-        if constexpr (RESET) rst = reset_mask<TPT>(p.reset, b, t0, L, lane);
-        copies_wait<0>();
-        __syncwarp();
-        float2 em1[TPT], u[TPT];
+    __syncthreads();
+    if (cl > 1) cluster_sync_all();  // every CTA's barriers exist before a peer completes on them
+
+    if (warp == NW) {
+        float2 carry = (active && p.init_state) ? *reinterpret_cast<const float2*>(p.init_state + b * C + c)
+                                                : dup(0.0f);
+        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+        bool ok = true;  // (whole-warp: no map is sent, received or waited for after a timeout)
+        for (int it = 0; it < rounds; ++it) {
+            const int buf = it & 1;
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            float4 g[NW];
+            uint32_t rst = 0;
 #pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            float2 r, i, a;
-            sigmas<EXACT>(TL::read(tiles + TL::kBytes, j, lane), TL::read(tiles + 2 * TL::kBytes, j, lane), r, i);
-            decays<EXACT>(mul2(k, r), em1[j], a);
-            float2 n = input_weight(em1[j]);
-            if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
-            u[j] = mul2(mul2(n, i), TL::read(tiles, j, lane));
-        }
-        __syncwarp();
-        if (tr + round < L) fetch(t0 + round);
-        // tokens past the end change nothing
-        if (t0 + TPT > L) {
-#pragma unroll
-            for (int j = 0; j < TPT; ++j)
-                if (t0 + j >= L) em1[j] = u[j] = dup(0.0f);
-        }
-        // the group's map
-        float2 A = dup(1.0f), H = dup(0.0f);
-#pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            if (RESET && ((rst >> j) & 1)) {
-                A = dup(0.0f);
-                H = u[j];
-            } else {
-                A = fma2(em1[j], A, A);
-                H = add2(H, fma2(em1[j], H, u[j]));
+            for (int w = 0; w < NW; ++w) {
+                g[w] = ex.group_map[w][lane];
+                if (RESET && ex.group_rst[w]) rst |= 1u << w;
             }
-        }
-        group_map[buf][warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        if (RESET && lane == 0) group_rst[buf][warp] = rst != 0;
-        __syncthreads();
-        // the state entering the group: carry, the tiles before, the groups before
-        float2 h = carry;
-        if (cl > 1) {
-            // warps 0 .. cl - 1 (twice around for clusters beyond NW) send the tile's map
-            float4 m = group_map[buf][0][lane];
-            int any = RESET ? group_rst[buf][0] : 0;
+            float2 h = carry;
+            if (cl > 1 && ok) {
+                float4 m = g[0];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                const float4 g = group_map[buf][w][lane];
-                const bool gr = RESET && group_rst[buf][w];
-                const float2 hh = apply(g, gr, make_float2(m.z, m.w));
-                const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g.x, g.y), make_float2(m.x, m.y));
-                m = make_float4(aa.x, aa.y, hh.x, hh.y);
-                any |= gr;
+                for (int w = 1; w < NW; ++w) {
+                    const bool gr = RESET && ((rst >> w) & 1);
+                    const float2 hh = apply(g[w], gr, make_float2(m.z, m.w));
+                    const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g[w].x, g[w].y), make_float2(m.x, m.y));
+                    m = make_float4(aa.x, aa.y, hh.x, hh.y);
+                }
+                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+                __syncwarp();
+                if (!(rank == 0 && it == withhold)) {
+                    for (int to = 0; to < cl; ++to)
+                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
+                    if (RESET && lane < cl)
+                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
+                }
+                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+                for (int q = 0; q < cl; ++q) {
+                    if (q == rank) h = carry;
+                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
+                }
             }
-            for (int to = warp; to < cl; to += NW) {
-                store_remote(&tile_map[buf][rank][lane], to, m);
-                if (RESET && lane == 0) store_remote(&tile_rst[buf][rank], to, any);
-            }
-            cluster_arrive();
-            cluster_wait();
-            for (int q = 0; q < cl; ++q) {
-                if (q == rank) h = carry;
-                carry = apply(tile_map[buf][q][lane], RESET && tile_rst[buf][q], carry);
-            }
-        }
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            if (w == warp && cl > 1) break;
-            const float2 v = apply(group_map[buf][w][lane], RESET && group_rst[buf][w], cl > 1 ? h : carry);
-            if (cl > 1) {
-                h = v;
-            } else {
-                if (w == warp) h = carry;
-                carry = v;
+            for (int w = 0; w < NW; ++w) {
+                ex.entering[w][lane] = h;
+                h = apply(g[w], RESET && ((rst >> w) & 1), h);
             }
+            if (cl == 1) carry = h;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
         }
-        if (active && p.states && t0 < L && t0 % kInterval == 0)
-            *reinterpret_cast<float2*>(p.states + (b * nst + t0 / kInterval) * C + c) = h;
+        if (p.final_state && active && rank == 0)
+            *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
+    } else {
+        int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
+        const int64_t nst = (L + kInterval - 1) / kInterval;
+        T* y = static_cast<T*>(p.y) + (b * L + t0) * C + c;
+        uint8_t* tiles = ring + warp * kStages * 3 * TL::kBytes;
+        // the lane's own 16-byte chunk of the group's first row
+        const int64_t cc = c0 + (lane % TL::kChunks) * TL::kElems;
+        const bool in = cc < C;
+        int64_t next = (b * L + t0 + lane / TL::kChunks) * C + cc;  // ... of the next round to fetch
+        auto rows_left = [&](int64_t t) { return t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t); };
+        // (an empty group of copies past the last round keeps the count)
+        auto fetch = [&](int it, int slot) {
+            if (it < rounds) {
+                const int left = rows_left(static_cast<int64_t>(it) * round + rank * TILE + warp * TPT);
+                uint8_t* dst = tiles + slot * 3 * TL::kBytes;
+                TL::load(dst, static_cast<const T*>(p.x) + next, left, in, C, lane);
+                TL::load(dst + TL::kBytes, static_cast<const T*>(p.gate_a) + next, left, in, C, lane);
+                TL::load(dst + 2 * TL::kBytes, static_cast<const T*>(p.gate_x) + next, left, in, C, lane);
+                next += round * C;
+            }
+            copies_commit();
+        };
 #pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            if (RESET && ((rst >> j) & 1)) h = u[j];
-            else h = add2(h, fma2(em1[j], h, u[j]));
-            if (active && t0 + j < L)
-                *reinterpret_cast<typename Pair<T>::Raw*>(y + (t0 + j) * C) = Pair<T>::narrow(h);
+        for (int s = 0; s < kStages; ++s) fetch(s, s);
+        const float2 k = decay_rates(p, c, active);
+        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+        bool ok = true;
+        for (int it = 0; it < rounds; ++it, t0 += round, y += round * C) {
+            const int slot = it % kStages;
+            uint32_t rst = 0;
+            if constexpr (RESET) rst = reset_mask<TPT>(p.reset, b, t0, L, lane);
+            copies_wait<kStages - 1>();
+            __syncwarp();
+            // the gates and the group's map
+            const uint8_t* src = tiles + slot * 3 * TL::kBytes;
+            float2 em1[TPT], u[TPT];
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                float2 r, i, a;
+                sigmas<EXACT>(TL::read(src + TL::kBytes, j, lane), TL::read(src + 2 * TL::kBytes, j, lane), r, i);
+                decays<EXACT>(mul2(k, r), slow, em1[j], a);
+                float2 n = input_weight(em1[j]);
+                if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
+                u[j] = mul2(mul2(n, i), TL::read(src, j, lane));
+            }
+            __syncwarp();
+            fetch(it + kStages, slot);
+            const int left = rows_left(t0);
+            if (left < TPT) {  // tokens past the end change nothing
+#pragma unroll
+                for (int j = 0; j < TPT; ++j)
+                    if (j >= left) em1[j] = u[j] = dup(0.0f);
+            }
+            float2 A = dup(1.0f), H = dup(0.0f);
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                if (RESET && ((rst >> j) & 1)) {
+                    A = dup(0.0f);
+                    H = u[j];
+                } else {
+                    A = fma2(em1[j], A, A);
+                    H = add2(H, fma2(em1[j], H, u[j]));
+                }
+            }
+            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+            // the outputs
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+            float2 h = ex.entering[warp][lane];
+            // a tile starts at a multiple of the interval: group 0 keeps its state
+            if (warp == 0 && p.states && active && left > 0)
+                *reinterpret_cast<float2*>(p.states + (b * nst + t0 / kInterval) * C + c) = h;
+            const int live = active ? left : 0;
+            T* yt = y;
+#pragma unroll
+            for (int j = 0; j < TPT; ++j, yt += C) {
+                if (RESET && ((rst >> j) & 1)) h = u[j];
+                else h = add2(h, fma2(em1[j], h, u[j]));
+                if (j < live) *reinterpret_cast<typename Pair<T>::Raw*>(yt) = Pair<T>::narrow(h);
+            }
         }
     }
-    if (p.final_state && active && rank == 0 && warp == 0)
-        *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
+    __syncthreads();
+    if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
+    if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
 }
 
 template <typename T>
@@ -344,7 +425,7 @@ __global__ void __launch_bounds__(128) gated_scan_bwd_kernel(GatedScanParams p) 
         sigmas<EXACT>(dup(to_f32(static_cast<const T*>(p.gate_a)[o])),
                       dup(to_f32(static_cast<const T*>(p.gate_x)[o])), r, i);
         la = mul2(dup(k), r);
-        decays<EXACT>(la, em1, a);
+        decays<EXACT>(la, false, em1, a);
         if (rs) {
             em1 = dup(-1.0f);
             a = dup(0.0f);
@@ -404,7 +485,7 @@ __global__ void __launch_bounds__(256) gated_update_kernel(GatedUpdateParams p) 
     const bool rs = p.reset && p.reset[i / p.channels];
     float2 r, ii, em1, a;
     sigmas<EXACT>(dup(to_f32(static_cast<const T*>(p.gate_a)[i])), dup(to_f32(static_cast<const T*>(p.gate_x)[i])), r, ii);
-    decays<EXACT>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), em1, a);
+    decays<EXACT>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), false, em1, a);
     if (rs) em1 = dup(-1.0f);
     const float h = p.state[i];
     const float hn = (rs ? 0.0f : fmaf(em1.x, h, h)) +
@@ -426,6 +507,7 @@ int device_sms() {
 // CTAs per cluster: the smallest power of two that gives every SM two CTAs, as
 // long as the sequence has tiles for them.
 int cluster_size(int64_t blocks, int64_t seqlen, int tile) {
+    if (const char* e = getenv("DEV_CL")) return atoi(e);
     int cl = 1;
     const int64_t want = 2 * static_cast<int64_t>(device_sms());
     while (cl < kMaxCluster && blocks * cl < want && static_cast<int64_t>(cl) * tile < seqlen) cl *= 2;
@@ -459,12 +541,12 @@ size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
 }
 
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
-    constexpr int TPT = kFwdTokens<T>;
     const int64_t blocks = (p.channels + CPB - 1) / CPB;
-    const int cl = cluster_size(blocks * p.batch, p.seqlen, NW * TPT);
-    const size_t smem = NW * 3 * Tile<T, TPT>::kBytes;
-    return p.reset ? launch_clusters(gated_scan_kernel<T, true>, blocks, p.batch, cl, smem, s, p, cl)
-                   : launch_clusters(gated_scan_kernel<T, false>, blocks, p.batch, cl, smem, s, p, cl);
+    const int cl = cluster_size(blocks * p.batch, p.seqlen, TILE);
+    const size_t smem = NW * kStages * 3 * Tile<T, TPT>::kBytes;
+    const int wh = static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP));
+    return p.reset ? launch_clusters(gated_scan_kernel<T, true>, blocks, p.batch, cl, smem, s, p, cl, wh)
+                   : launch_clusters(gated_scan_kernel<T, false>, blocks, p.batch, cl, smem, s, p, cl, wh);
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {
@@ -480,6 +562,15 @@ template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p
     const int64_t n = p.batch * p.channels;
     return launch_kernel(gated_update_kernel<T>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
                          0, s, true, p);
+}
+
+cudaError_t gated_scan_take_status(int* v, cudaStream_t s) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_gated_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbolAsync(g_gated_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return e;
 }
 
 template cudaError_t launch_gated_scan<float>(const GatedScanParams&, cudaStream_t);

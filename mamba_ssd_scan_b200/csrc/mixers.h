@@ -45,6 +45,8 @@ struct GatedUpdateParams {
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s);
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s);
 template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p, cudaStream_t s);
+// Copies the scan's device status word to *v and clears it (synchronises s).
+cudaError_t gated_scan_take_status(int* v, cudaStream_t s);
 // Bytes of the backward's partial sums.
 size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels);
 
