@@ -21,7 +21,7 @@
 #include <stdlib.h>
 #include "mixers.h"
 #include "tcgen05.cuh"
-#include "tma.cuh"
+#include "rows_tma.cuh"
 #include "vec16.cuh"
 
 namespace ssd {
@@ -68,23 +68,38 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// 2^(k v) for a constant k = hi + lo in two parts, cut off at 2^top.  For fp32
-// inputs the rounding of k v (up to 2^-24 |k v| in the exponent) is carried
-// along; for bf16 inputs it stays well inside their own 2^-9.
+// 2^(k v) for a constant k = hi + lo in two parts.  For fp32 inputs (EXACT) it is
+// cut off at 2^top and the rounding of k v (up to 2^-24 |k v| in the exponent)
+// is carried along; for bf16 inputs that rounding stays well inside their own
+// 2^-9, and the gates are cut off as they are read.
 template <bool EXACT>
 __device__ __forceinline__ float2 exp2_scaled(float2 v, float hi, float lo, float top = 126.0f) {
-    if constexpr (EXACT)  // no infinite products below
+    if constexpr (EXACT) {  // (no infinite products)
         v = make_float2(min_nan(max_nan(v.x, -200.0f), 200.0f), min_nan(max_nan(v.y, -200.0f), 200.0f));
-    const float2 t = mul2(v, dup(hi));
-    float2 e = make_float2(ex2_approx(min_nan(t.x, top)), ex2_approx(min_nan(t.y, top)));
-    if constexpr (EXACT) {
+        const float2 t = mul2(v, dup(hi));
+        const float2 e = make_float2(ex2_approx(min_nan(t.x, top)), ex2_approx(min_nan(t.y, top)));
         const float2 d = fma2(v, dup(lo), fma2(v, dup(hi), make_float2(-t.x, -t.y)));  // what t lost
-        e = fma2(e, mul2(d, dup(0.69314718f)), e);
+        return fma2(e, mul2(d, dup(0.69314718f)), e);
     }
-    return e;
+    const float2 t = mul2(v, dup(hi));
+    return make_float2(ex2_approx(t.x), ex2_approx(t.y));
 }
 // log2(e) in two parts
 constexpr float kLog2eHi = 1.44269502162933349609375f, kLog2eLo = 1.9259629911266174e-8f;
+
+// A pair of gates as it lies in memory; bf16 gates no lower than `least` (two
+// equal halves; NaN stays), which bounds e^-gate.
+__device__ __forceinline__ float2 read_gates(float2 raw, uint32_t) { return raw; }
+__device__ __forceinline__ float2 read_gates(uint32_t raw, uint32_t least) {
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(raw) : "r"(least));
+    return Pair<__nv_bfloat16>::widen(raw);
+}
+// one widened gate, cut off alike
+template <bool EXACT> __device__ __forceinline__ float2 one_gate(float v, float least) {
+    return dup(EXACT ? v : max_nan(v, least));
+}
+constexpr uint32_t kLeastA = 0xC2AEC2AEu;  // -87: e^87 < 2^126
+constexpr uint32_t kLeastX = 0xC226C226u;  // -41.5: e^41.5 < 2^60
 
 // sigma of a pair of gates with one reciprocal per channel:
 // 1 / ((1 + e^-a)(1 + e^-x)) times the other factor (a reciprocal each would
@@ -188,42 +203,9 @@ __device__ __forceinline__ bool wait_cluster(uint32_t mbar, uint32_t parity, vol
 // cleared by ssd_gated_scan_check_status.
 __device__ int g_gated_status;
 
-// ---- a warp's tile of one array: TPT rows of 64 channels, by 16-byte copies ----
-template <typename T, int TPT> struct Tile {
-    static constexpr int kRowBytes = CPB * sizeof(T);
-    static constexpr int kBytes = TPT * kRowBytes;
-    static constexpr int kChunks = kRowBytes / 16;          // per row
-    static constexpr int kRows = 32 / kChunks;              // rows per copy instruction
-    static constexpr int kElems = 16 / static_cast<int>(sizeof(T));
-    // rows 0 .. TPT - 1 of the array whose row 0 the lane's own chunk starts at src (row
-    // stride C elements); rows from `left` on and, without `in`, all of the lane's chunks read as zero
-    static __device__ __forceinline__ void load(uint8_t* dst, const T* src, int left, bool in, int64_t C, int lane) {
-        uint32_t s = static_cast<uint32_t>(__cvta_generic_to_shared(dst)) + lane * 16;
-        const int n = in ? left - lane / kChunks : 0;  // rows of this lane's column of chunks
-#pragma unroll
-        for (int k = 0; k < TPT / kRows; ++k) {
-            const bool on = k * kRows < n;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                         :
-                         : "r"(s + k * 512), "l"(on ? src + k * kRows * C : nullptr), "r"(on ? 16 : 0)
-                         : "memory");
-        }
-    }
-    static __device__ __forceinline__ float2 read(const uint8_t* t, int row, int lane) {
-        using Raw = typename Pair<T>::Raw;
-        return Pair<T>::widen(*reinterpret_cast<const Raw*>(t + row * kRowBytes + lane * sizeof(Raw)));
-    }
-};
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" : : "n"(N) : "memory");
-}
-
-// restarts among the group's tokens, bit j = token t0 + j
-template <int TPT>
-__device__ __forceinline__ uint32_t reset_mask(const uint8_t* reset, int64_t row, int64_t t0, int64_t L, int lane) {
-    const bool on = lane < TPT && t0 + lane < L && reset[row * L + t0 + lane] != 0;
-    return __ballot_sync(0xffffffffu, on);
+// restarts among the group's tokens: lane j's flag of token t0 + j
+__device__ __forceinline__ bool reset_flag(const uint8_t* reset, int64_t row, int64_t t0, int64_t L, int lane) {
+    return lane < TPT && t0 + lane < L && reset[row * L + t0 + lane] != 0;
 }
 
 // the composition of a map with a state; a map with a restart inside forgets
@@ -238,18 +220,28 @@ struct Exchange {
     float4 tile_map[2][kMaxCluster][32];  // the cluster's tiles, two rounds
     float2 entering[NW][32];              // the state entering each group
     int group_rst[NW], tile_rst[2][kMaxCluster];
-    uint64_t maps_ready, states_ready, tiles_ready[2];
+    uint64_t maps_ready, states_ready, tiles_ready[2], loaded[NW][2];
     int abort;
 };
 
-// 16-byte copies in flight ahead of the arithmetic, in groups of tokens
-constexpr int kStages = 2;
+// A warp's ring of input tiles (TPT rows of 64 channels): two rounds ahead for
+// bf16; one for fp32, whose tiles are twice as large, so that three CTAs still
+// share an SM.
+template <typename T> constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+template <typename T> constexpr int kRowBytes = CPB * sizeof(T);
+template <typename T> constexpr int kTileBytes = TPT * kRowBytes<T>;
+
+struct ScanMaps {
+    CUtensorMap x, gate_a, gate_x, y;
+};
 
 template <typename T, bool RESET>
-__global__ void __launch_bounds__(TPB, 3) gated_scan_kernel(GatedScanParams p, int cl, int withhold) {
+__global__ void __launch_bounds__(TPB, 3)
+    gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
-    using TL = Tile<T, TPT>;
-    extern __shared__ __align__(16) uint8_t ring[];    // [NW][kStages][3] tiles
+    constexpr int ST = kStages<T>, TB = kTileBytes<T>;
+    using Raw = typename Pair<T>::Raw;
+    extern __shared__ __align__(128) uint8_t ring[];    // [NW][ST][3] tiles: x, gate_x, gate_a (then y)
     __shared__ Exchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
@@ -263,6 +255,11 @@ __global__ void __launch_bounds__(TPB, 3) gated_scan_kernel(GatedScanParams p, i
         tc::mbar_init(tc::smem_u32(&ex.states_ready), 1);
         tc::mbar_init(tc::smem_u32(&ex.tiles_ready[0]), 1);
         tc::mbar_init(tc::smem_u32(&ex.tiles_ready[1]), 1);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            tc::mbar_init(tc::smem_u32(&ex.loaded[w][0]), 1);
+            tc::mbar_init(tc::smem_u32(&ex.loaded[w][1]), 1);
+        }
         tc::fence_mbar_init();
         ex.abort = 0;
     }
@@ -324,51 +321,65 @@ __global__ void __launch_bounds__(TPB, 3) gated_scan_kernel(GatedScanParams p, i
     } else {
         int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
         const int64_t nst = (L + kInterval - 1) / kInterval;
-        T* y = static_cast<T*>(p.y) + (b * L + t0) * C + c;
-        uint8_t* tiles = ring + warp * kStages * 3 * TL::kBytes;
-        // the lane's own 16-byte chunk of the group's first row
-        const int64_t cc = c0 + (lane % TL::kChunks) * TL::kElems;
-        const bool in = cc < C;
-        int64_t next = (b * L + t0 + lane / TL::kChunks) * C + cc;  // ... of the next round to fetch
-        auto rows_left = [&](int64_t t) { return t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t); };
-        // (an empty group of copies past the last round keeps the count)
-        auto fetch = [&](int it, int slot) {
-            if (it < rounds) {
-                const int left = rows_left(static_cast<int64_t>(it) * round + rank * TILE + warp * TPT);
-                uint8_t* dst = tiles + slot * 3 * TL::kBytes;
-                TL::load(dst, static_cast<const T*>(p.x) + next, left, in, C, lane);
-                TL::load(dst + TL::kBytes, static_cast<const T*>(p.gate_a) + next, left, in, C, lane);
-                TL::load(dst + 2 * TL::kBytes, static_cast<const T*>(p.gate_x) + next, left, in, C, lane);
-                next += round * C;
-            }
-            copies_commit();
+        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
+        // lane 0 loads round n's tiles into their slot: x and gate_x, which
+        // arms the slot's barrier for all three, and gate_a, whose place holds y
+        // until its store has read it
+        auto load_x = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+            const int t = static_cast<int>(t0 + n * round);
+            tc::mbar_expect_tx(bar, 3 * TB);
+            tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
         };
-#pragma unroll
-        for (int s = 0; s < kStages; ++s) fetch(s, s);
+        auto load_a = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
+                              static_cast<int>(t0 + n * round), static_cast<int>(b));
+        };
+        if (lane == 0) {
+            for (int n = 0; n < ST && n < rounds; ++n) {
+                load_x(n);
+                load_a(n);
+            }
+        }
         const float2 k = decay_rates(p, c, active);
         const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+        const int64_t first = t0;
         bool ok = true;
-        for (int it = 0; it < rounds; ++it, t0 += round, y += round * C) {
-            const int slot = it % kStages;
+        bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
+        for (int it = 0; it < rounds; ++it) {
+            const int64_t t = first + it * round;
+            const int slot = it % ST;
+            const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
             uint32_t rst = 0;
-            if constexpr (RESET) rst = reset_mask<TPT>(p.reset, b, t0, L, lane);
-            copies_wait<kStages - 1>();
-            __syncwarp();
+            if constexpr (RESET) {
+                rst = __ballot_sync(0xffffffffu, flag);
+                flag = reset_flag(p.reset, b, t + round, L, lane);
+            }
+            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
             // the gates and the group's map
-            const uint8_t* src = tiles + slot * 3 * TL::kBytes;
             float2 em1[TPT], u[TPT];
 #pragma unroll
             for (int j = 0; j < TPT; ++j) {
+                const uint8_t* row = src + j * kRowBytes<T>;
                 float2 r, i, a;
-                sigmas<EXACT>(TL::read(src + TL::kBytes, j, lane), TL::read(src + 2 * TL::kBytes, j, lane), r, i);
+                sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
+                              read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
                 decays<EXACT>(mul2(k, r), slow, em1[j], a);
                 float2 n = input_weight(em1[j]);
                 if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
-                u[j] = mul2(mul2(n, i), TL::read(src, j, lane));
+                u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
             }
             __syncwarp();
-            fetch(it + kStages, slot);
-            const int left = rows_left(t0);
+            if (lane == 0) {
+                if (ST == 2 && it > 0 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();  // the previous round's y has left
+                    load_a(it + 1);
+                }
+                if (it + ST < rounds) load_x(it + ST);
+            }
+            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
             if (left < TPT) {  // tokens past the end change nothing
 #pragma unroll
                 for (int j = 0; j < TPT; ++j)
@@ -389,21 +400,33 @@ __global__ void __launch_bounds__(TPB, 3) gated_scan_kernel(GatedScanParams p, i
             if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-            // the outputs
+            // the outputs, over gate_a's tile, and out
             if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
             float2 h = ex.entering[warp][lane];
             // a tile starts at a multiple of the interval: group 0 keeps its state
             if (warp == 0 && p.states && active && left > 0)
-                *reinterpret_cast<float2*>(p.states + (b * nst + t0 / kInterval) * C + c) = h;
-            const int live = active ? left : 0;
-            T* yt = y;
+                *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
 #pragma unroll
-            for (int j = 0; j < TPT; ++j, yt += C) {
+            for (int j = 0; j < TPT; ++j) {
                 if (RESET && ((rst >> j) & 1)) h = u[j];
                 else h = add2(h, fma2(em1[j], h, u[j]));
-                if (j < live) *reinterpret_cast<typename Pair<T>::Raw*>(yt) = Pair<T>::narrow(h);
+                *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
+            }
+            tc::fence_smem_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (left > 0) {
+                    tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
+                                       static_cast<int>(t), static_cast<int>(b));
+                    tc::bulk_commit_group();
+                }
+                if (ST == 1 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();
+                    load_a(it + 1);
+                }
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
     }
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
@@ -422,8 +445,8 @@ __global__ void __launch_bounds__(128) gated_scan_bwd_kernel(GatedScanParams p) 
     float carry = p.d_final ? p.d_final[b * C + c] : 0.0f;  // a_{t+1} g_{t+1}
     float sum = 0.0f;
     auto gate = [&](int64_t o, bool rs, float2& r, float2& i, float2& la, float2& em1, float2& a, float2& n) {
-        sigmas<EXACT>(dup(to_f32(static_cast<const T*>(p.gate_a)[o])),
-                      dup(to_f32(static_cast<const T*>(p.gate_x)[o])), r, i);
+        sigmas<EXACT>(one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_a)[o]), -87.0f),
+                      one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_x)[o]), -41.5f), r, i);
         la = mul2(dup(k), r);
         decays<EXACT>(la, false, em1, a);
         if (rs) {
@@ -484,7 +507,8 @@ __global__ void __launch_bounds__(256) gated_update_kernel(GatedUpdateParams p) 
     grid_dep_launch();
     const bool rs = p.reset && p.reset[i / p.channels];
     float2 r, ii, em1, a;
-    sigmas<EXACT>(dup(to_f32(static_cast<const T*>(p.gate_a)[i])), dup(to_f32(static_cast<const T*>(p.gate_x)[i])), r, ii);
+    sigmas<EXACT>(one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_a)[i]), -87.0f),
+                  one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_x)[i]), -41.5f), r, ii);
     decays<EXACT>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), false, em1, a);
     if (rs) em1 = dup(-1.0f);
     const float h = p.state[i];
@@ -543,10 +567,17 @@ size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
     const int64_t blocks = (p.channels + CPB - 1) / CPB;
     const int cl = cluster_size(blocks * p.batch, p.seqlen, TILE);
-    const size_t smem = NW * kStages * 3 * Tile<T, TPT>::kBytes;
+    const size_t smem = NW * kStages<T> * 3 * kTileBytes<T>;
     const int wh = static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP));
-    return p.reset ? launch_clusters(gated_scan_kernel<T, true>, blocks, p.batch, cl, smem, s, p, cl, wh)
-                   : launch_clusters(gated_scan_kernel<T, false>, blocks, p.batch, cl, smem, s, p, cl, wh);
+    ScanMaps m;
+    const bool bf16 = sizeof(T) == 2;
+    if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, TPT) ||
+        !make_tmap_rows(&m.gate_a, p.gate_a, bf16, p.channels, p.seqlen, p.batch, TPT) ||
+        !make_tmap_rows(&m.gate_x, p.gate_x, bf16, p.channels, p.seqlen, p.batch, TPT) ||
+        !make_tmap_rows(&m.y, p.y, bf16, p.channels, p.seqlen, p.batch, TPT))
+        return cudaErrorInvalidValue;
+    return p.reset ? launch_clusters(gated_scan_kernel<T, true>, blocks, p.batch, cl, smem, s, p, m, cl, wh)
+                   : launch_clusters(gated_scan_kernel<T, false>, blocks, p.batch, cl, smem, s, p, m, cl, wh);
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {

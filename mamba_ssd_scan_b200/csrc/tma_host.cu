@@ -1,5 +1,5 @@
 // tma_host.cu -- host side of the TMA loads: encoding tiled tensor maps.
-#include "tma.cuh"
+#include "rows_tma.cuh"
 
 namespace ssd {
 namespace {
@@ -49,6 +49,21 @@ bool make_tmap_f32_2d(CUtensorMap* map, const void* base, uint64_t d0, uint64_t 
     const cuuint32_t estr[2] = {1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_tmap_rows(CUtensorMap* map, const void* base, bool bf16, uint64_t channels, uint64_t rows,
+                    uint64_t batch, uint32_t box1) {
+    EncodeTiledFn fn = encoder();
+    const uint64_t elt = bf16 ? 2 : 4;
+    if (!fn || box1 == 0 || box1 > 256 || channels * elt % 16 != 0) return false;
+    const cuuint64_t dims[3] = {channels, rows, batch};
+    const cuuint64_t strides[2] = {channels * elt, rows * channels * elt};
+    const cuuint32_t box[3] = {64, box1, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
