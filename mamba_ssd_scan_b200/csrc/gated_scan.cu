@@ -19,6 +19,8 @@
 // cluster.  Every mbarrier wait is bounded: on expiry the CTA raises its abort
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
 #include <stdlib.h>
+#include <utility>
+
 #include "mixers.h"
 #include "tcgen05.cuh"
 #include "rows_tma.cuh"
@@ -54,6 +56,11 @@ __device__ __forceinline__ float rcp_approx(float v) {
 __device__ __forceinline__ float sqrt_approx(float v) {
     float r;
     asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rsqrt_approx(float v) {
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
 // min and max that keep a NaN
@@ -433,60 +440,264 @@ __global__ void __launch_bounds__(TPB, 3)
     if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
 }
 
-template <typename T>
-__global__ void __launch_bounds__(128) gated_scan_bwd_kernel(GatedScanParams p) {
+// The gradient, the same way from the last token to the first: a group also has
+// the map of the adjoint it passes on, c <- a (dy + c) token by token backwards,
+// whose factor is the same A.  The state entering a tile is the forward's (a
+// tile is one interval), so only the adjoint crosses tiles.  The 8 warps form
+// both maps, the ninth hands each group its entering state and adjoint, and
+// the group is replayed, forwards for the states and backwards for the
+// outputs, which take the places of x, gate_x and gate_a in shared memory.
+struct ExchangeBwd {
+    float4 group_map[NW][32];             // A, H
+    float2 group_rev[NW][32];             // G: c out = A c in + G
+    float4 tile_map[2][kMaxCluster][32];  // A, G of the cluster's tiles, two rounds
+    float4 entering[NW][32];              // the state and the adjoint entering each group
+    int group_rst[NW], tile_rst[2][kMaxCluster];
+    uint64_t maps_ready, states_ready, tiles_ready[2], loaded[NW][2];
+    int abort;
+};
+
+template <typename T> constexpr int kStagesBwd = sizeof(T) == 2 ? 2 : 1;
+
+struct ScanBwdMaps {
+    CUtensorMap x, gate_a, gate_x, dy, dx, dgate_a, dgate_x;
+};
+
+template <typename T, bool RESET>
+__global__ void __launch_bounds__(TPB, 2)
+    gated_scan_bwd_kernel(GatedScanParams p, const __grid_constant__ ScanBwdMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
-    const int64_t C = p.channels, L = p.seqlen;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t b = blockIdx.y;
-    if (c >= C) return;
-    const float k = -p.scale * softplus_f32(p.decay[c]);
-    const int64_t nst = (L + kInterval - 1) / kInterval;
-    float carry = p.d_final ? p.d_final[b * C + c] : 0.0f;  // a_{t+1} g_{t+1}
-    float sum = 0.0f;
-    auto gate = [&](int64_t o, bool rs, float2& r, float2& i, float2& la, float2& em1, float2& a, float2& n) {
-        sigmas<EXACT>(one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_a)[o]), -87.0f),
-                      one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_x)[o]), -41.5f), r, i);
-        la = mul2(dup(k), r);
-        decays<EXACT>(la, false, em1, a);
-        if (rs) {
-            em1 = dup(-1.0f);
-            a = dup(0.0f);
+    constexpr int ST = kStagesBwd<T>, TB = kTileBytes<T>;
+    using Raw = typename Pair<T>::Raw;
+    extern __shared__ __align__(128) uint8_t ring[];    // [NW][ST][4] tiles: x, gate_x, gate_a, dy
+    __shared__ ExchangeBwd ex;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
+    const int rank = static_cast<int>(blockIdx.x) % cl;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x / cl) * CPB, c = c0 + 2 * lane;
+    const bool active = c < C;
+    const int64_t round = static_cast<int64_t>(cl) * TILE;
+    const int rounds = static_cast<int>((L + round - 1) / round);
+    if (threadIdx.x == 0) {
+        tc::mbar_init(tc::smem_u32(&ex.maps_ready), NW);
+        tc::mbar_init(tc::smem_u32(&ex.states_ready), 1);
+        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[0]), 1);
+        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[1]), 1);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            tc::mbar_init(tc::smem_u32(&ex.loaded[w][0]), 1);
+            tc::mbar_init(tc::smem_u32(&ex.loaded[w][1]), 1);
         }
-        n = input_weight(em1);
-    };
-    for (int64_t st = nst - 1; st >= 0; --st) {
-        float hp[kInterval];
-        float h = p.states[(b * nst + st) * C + c];
-        const int64_t t0 = st * kInterval;
-        const int n = static_cast<int>(L - t0 < kInterval ? L - t0 : kInterval);
-        for (int j = 0; j < n; ++j) {
-            const int64_t o = (b * L + t0 + j) * C + c;
-            const bool rs = p.reset && p.reset[b * L + t0 + j];
-            float2 r, i, la, em1, a, nn;
-            gate(o, rs, r, i, la, em1, a, nn);
-            hp[j] = h;
-            h = (rs ? 0.0f : fmaf(em1.x, h, h)) + nn.x * (i.x * to_f32(static_cast<const T*>(p.x)[o]));
-        }
-        for (int j = n - 1; j >= 0; --j) {
-            const int64_t o = (b * L + t0 + j) * C + c;
-            const bool rs = p.reset && p.reset[b * L + t0 + j];
-            float2 r, i, la, em1, a, nn;
-            gate(o, rs, r, i, la, em1, a, nn);
-            const float x = to_f32(static_cast<const T*>(p.x)[o]);
-            const float gt = to_f32(static_cast<const T*>(p.dy)[o]) + carry;
-            const float ix = i.x * x;
-            static_cast<T*>(p.dx)[o] = from_f32<T>(gt * nn.x * i.x);
-            static_cast<T*>(p.dgate_x)[o] = from_f32<T>(gt * nn.x * ix * (1.0f - i.x));
-            // a decay of exactly 1 (n = 0) passes a finite dla times la = 0
-            const float dla = rs ? 0.0f : gt * a.x * (hp[j] - a.x / fmaxf(nn.x, 1e-18f) * ix);
-            static_cast<T*>(p.dgate_a)[o] = from_f32<T>(dla * la.x * (1.0f - r.x));
-            sum = fmaf(dla, r.x, sum);
-            carry = rs ? 0.0f : fmaf(em1.x, gt, gt);
-        }
+        tc::fence_mbar_init();
+        ex.abort = 0;
     }
-    if (p.d_init) p.d_init[b * C + c] = carry;
-    p.partial[b * C + c] = sum;
+    __syncthreads();
+    if (cl > 1) cluster_sync_all();
+    float2 sum = dup(0.0f);
+
+    if (warp == NW) {
+        const int64_t nst = (L + kInterval - 1) / kInterval;
+        // the kept state entering this CTA's tile of a round (rounds run backwards)
+        auto kept = [&](int it) {
+            const int64_t tile = static_cast<int64_t>(rounds - 1 - it) * cl + rank;
+            return active && it < rounds && tile < nst
+                       ? *reinterpret_cast<const float2*>(p.states + (b * nst + tile) * C + c)
+                       : dup(0.0f);
+        };
+        float2 carry = (active && p.d_final) ? *reinterpret_cast<const float2*>(p.d_final + b * C + c) : dup(0.0f);
+        float2 next = kept(0);
+        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+        bool ok = true;
+        for (int it = 0; it < rounds; ++it) {
+            const int buf = it & 1;
+            float2 h = next;
+            next = kept(it + 1);
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            float2 A[NW], G[NW];
+            uint32_t rst = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 g = ex.group_map[w][lane];
+                A[w] = make_float2(g.x, g.y);
+                G[w] = ex.group_rev[w][lane];
+                if (RESET && ex.group_rst[w]) rst |= 1u << w;
+                *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
+                h = apply(g, RESET && ((rst >> w) & 1), h);
+            }
+            auto step = [&](int w, float2 v) { return RESET && ((rst >> w) & 1) ? G[w] : fma2(A[w], v, G[w]); };
+            float2 cin = carry;
+            if (cl > 1 && ok) {
+                float2 a = A[NW - 1], g = G[NW - 1];
+#pragma unroll
+                for (int w = NW - 2; w >= 0; --w) {
+                    g = step(w, g);
+                    a = RESET && ((rst >> w) & 1) ? dup(0.0f) : mul2(A[w], a);
+                }
+                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+                __syncwarp();
+                if (!(rank == 0 && it == withhold)) {
+                    for (int to = 0; to < cl; ++to)
+                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), make_float4(a.x, a.y, g.x, g.y),
+                                    in_rank(&ex.tiles_ready[buf], to));
+                    if (RESET && lane < cl)
+                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
+                }
+                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+                for (int q = cl - 1; q >= 0; --q) {
+                    if (q == rank) cin = carry;
+                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
+                }
+            }
+#pragma unroll
+            for (int w = NW - 1; w >= 0; --w) {
+                *(reinterpret_cast<float2*>(&ex.entering[w][lane]) + 1) = cin;
+                cin = step(w, cin);
+            }
+            if (cl == 1) carry = cin;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+        }
+        if (p.d_init && active && rank == 0) *reinterpret_cast<float2*>(p.d_init + b * C + c) = carry;
+    } else {
+        const int64_t first = static_cast<int64_t>(rank) * TILE + warp * TPT;
+        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 4 * TB;
+        const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
+        auto token = [&](int it) { return first + static_cast<int64_t>(rounds - 1 - it) * round; };
+        auto load = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 4 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+            const int t = static_cast<int>(token(n));
+            tc::mbar_expect_tx(bar, 4 * TB);
+            tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
+            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, ci, t, bi);
+            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, ci, t, bi);
+            tc::tma_load_rows(dst + 3 * TB, &maps.dy, bar, ci, t, bi);
+        };
+        if (lane == 0)
+            for (int n = 0; n < ST && n < rounds; ++n) load(n);
+        const float2 k = decay_rates(p, c, active);
+        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+        bool ok = true;
+        bool flag = RESET && reset_flag(p.reset, b, token(0), L, lane);
+        for (int it = 0; it < rounds; ++it) {
+            const int64_t t = token(it);
+            const int slot = it % ST;
+            uint8_t* src = ring + (warp * ST + slot) * 4 * TB + lane * sizeof(Raw);
+            auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * TB + j * kRowBytes<T>); };
+            uint32_t rst = 0;
+            if constexpr (RESET) {
+                rst = __ballot_sync(0xffffffffu, flag);
+                flag = it + 1 < rounds && reset_flag(p.reset, b, t - round, L, lane);
+            }
+            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
+            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+            float2 r[TPT], i[TPT], em1[TPT];
+            float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                float2 a;
+                sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
+                decays<EXACT>(mul2(k, r[j]), slow, em1[j], a);
+                float2 n = input_weight(em1[j]);
+                const bool rs = RESET && ((rst >> j) & 1);
+                if (rs) n = dup(1.0f);
+                float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+                if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
+                if (rs) {
+                    A = dup(0.0f);
+                    H = u;
+                } else {
+                    A = fma2(em1[j], A, A);
+                    H = add2(H, fma2(em1[j], H, u));
+                }
+            }
+#pragma unroll
+            for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
+                G = add2(G, Pair<T>::widen(*at(3, j)));
+                G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
+            }
+            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+            ex.group_rev[warp][lane] = G;
+            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+                if (ST == 2 && it > 0 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();  // the previous round's outputs have left
+                    load(it + 1);
+                }
+            }
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+            const float4 in = ex.entering[warp][lane];
+            float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
+            float2 hp[TPT];
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                hp[j] = h;
+                const bool rs = RESET && ((rst >> j) & 1);
+                const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
+                const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+                h = rs ? u : add2(h, fma2(em1[j], h, u));
+            }
+#pragma unroll
+            for (int j = TPT - 1; j >= 0; --j) {
+                const bool rs = RESET && ((rst >> j) & 1);
+                const float2 x = Pair<T>::widen(*at(0, j));
+                g = add2(g, Pair<T>::widen(*at(3, j)));
+                const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
+                float2 a = add2(em1[j], dup(1.0f));
+                if (!slow) {  // a small decay as it is, not as 1 + em1
+                    const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
+                    if (!(la.x >= -0.25f)) a.x = e.x;
+                    if (!(la.y >= -0.25f)) a.y = e.y;
+                }
+                // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
+                // gives a finite dla, times la = 0
+                const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
+                const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
+                const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
+                const float2 dx = mul2(mul2(g, n), i[j]);
+                const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
+                float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
+                if (rs) dla = dup(0.0f);
+                const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
+                if (j < left) sum = fma2(dla, r[j], sum);
+                g = rs ? dup(0.0f) : fma2(em1[j], g, g);
+                *at(0, j) = Pair<T>::narrow(dx);
+                *at(1, j) = Pair<T>::narrow(dgx);
+                *at(2, j) = Pair<T>::narrow(dga);
+            }
+            tc::fence_smem_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (left > 0) {
+                    const uint32_t out = tiles + slot * 4 * TB;
+                    tc::tma_store_rows(&maps.dx, out, ci, static_cast<int>(t), bi);
+                    tc::tma_store_rows(&maps.dgate_x, out + TB, ci, static_cast<int>(t), bi);
+                    tc::tma_store_rows(&maps.dgate_a, out + 2 * TB, ci, static_cast<int>(t), bi);
+                    tc::bulk_commit_group();
+                }
+                if (ST == 1 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();
+                    load(it + 1);
+                }
+            }
+        }
+        if (lane == 0) tc::bulk_wait_all();
+    }
+    // the CTA's sums of dla r, group after group
+    __syncthreads();
+    if (warp < NW) *reinterpret_cast<float2*>(&ex.entering[warp][lane]) = sum;
+    __syncthreads();
+    if (warp == 0 && active) {
+        float2 s = dup(0.0f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s = add2(s, *reinterpret_cast<float2*>(&ex.entering[w][lane]));
+        *reinterpret_cast<float2*>(p.partial + (b * cl + rank) * C + c) = s;
+    }
+    if (cl > 1) cluster_sync_all();
+    if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
 }
 
 // ddecay = -scale * sigma(decay) * the sum of dla * r over batch and time
@@ -561,7 +772,7 @@ cudaError_t launch_clusters(Kern kern, int64_t blocks, int64_t batch, int cl, si
 }  // namespace
 
 size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
-    return static_cast<size_t>(batch) * channels * sizeof(float);
+    return static_cast<size_t>(batch) * kMaxCluster * channels * sizeof(float);
 }
 
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
@@ -581,12 +792,23 @@ template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cu
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {
-    const dim3 grid(static_cast<unsigned>((p.channels + 127) / 128), static_cast<unsigned>(p.batch));
-    gated_scan_bwd_kernel<T><<<grid, 128, 0, s>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const int64_t blocks = (p.channels + CPB - 1) / CPB;
+    const int cl = cluster_size(blocks * p.batch, p.seqlen, TILE);
+    const size_t smem = NW * kStagesBwd<T> * 4 * kTileBytes<T>;
+    const int wh = static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP));
+    ScanBwdMaps m;
+    const std::pair<CUtensorMap*, const void*> arrays[] = {
+        {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.dy, p.dy},
+        {&m.dx, p.dx}, {&m.dgate_a, p.dgate_a}, {&m.dgate_x, p.dgate_x}};
+    for (const auto& a : arrays)
+        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TPT))
+            return cudaErrorInvalidValue;
+    const cudaError_t e =
+        p.reset ? launch_clusters(gated_scan_bwd_kernel<T, true>, blocks, p.batch, cl, smem, s, p, m, cl, wh)
+                : launch_clusters(gated_scan_bwd_kernel<T, false>, blocks, p.batch, cl, smem, s, p, m, cl, wh);
     if (e != cudaSuccess) return e;
     return launch_kernel(gated_scan_finish_kernel, dim3(static_cast<unsigned>((p.channels + 31) / 32)),
-                         dim3(kColSumThreads), 0, s, true, p, p.batch);
+                         dim3(kColSumThreads), 0, s, true, p, p.batch * cl);
 }
 
 template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p, cudaStream_t s) {
