@@ -9,12 +9,12 @@
 // registers, while the gates (about 4 special-function results per element)
 // are formed once and the inputs are read once.
 //
-// A compute warp takes one group of tokens of 64 channels (a pair per lane);
-// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens),
-// and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
-// tile's map, sends it to the cluster's CTAs through distributed shared memory
-// (asynchronous stores that complete on the receiver's mbarrier), and hands
-// each group its entering state.  The order of composition is fixed, so
+// A warp takes one group of tokens of 64 channels (a pair per lane); the 8
+// warps of a CTA take consecutive groups (a tile of 64 tokens), and the CTAs of
+// a cluster consecutive tiles.  Warp 0 composes the tile's map, sends it to the
+// cluster's CTAs through distributed shared memory (asynchronous stores that
+// complete on the receiver's mbarrier), and hands each group its entering
+// state.  The order of composition is fixed, so
 // results do not depend on timing; there is no workspace and no wait on another
 // cluster.  Every mbarrier wait is bounded: on expiry the CTA raises its abort
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
@@ -30,8 +30,8 @@ namespace ssd {
 namespace {
 
 constexpr int kInterval = SSD_GATED_SCAN_INTERVAL;
-constexpr int NW = 8;            // compute warps (groups) per CTA
-constexpr int TPB = (NW + 1) * 32;
+constexpr int NW = 8;            // warps (groups) per CTA
+constexpr int TPB = NW * 32;
 constexpr int TPT = 8;           // tokens per group
 constexpr int TILE = NW * TPT;   // tokens per CTA and round
 static_assert(TILE == kInterval, "a tile starts where a state is kept");
@@ -273,168 +273,164 @@ __global__ void __launch_bounds__(TPB, 3)
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // every CTA's barriers exist before a peer completes on them
 
-    if (warp == NW) {
-        float2 carry = (active && p.init_state) ? *reinterpret_cast<const float2*>(p.init_state + b * C + c)
-                                                : dup(0.0f);
-        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
-        bool ok = true;  // (whole-warp: no map is sent, received or waited for after a timeout)
-        for (int it = 0; it < rounds; ++it) {
-            const int buf = it & 1;
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
-            ok = __all_sync(0xffffffffu, ok);
-            float4 g[NW];
-            uint32_t rst = 0;
+    // warp 0's part in a round (false once a wait has given up: no map is then
+    // sent, received or waited for)
+    float2 carry = (warp == 0 && active && p.init_state)
+                       ? *reinterpret_cast<const float2*>(p.init_state + b * C + c) : dup(0.0f);
+    const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+    auto hand_out = [&](int it, bool ok) {
+        const int buf = it & 1;
+        if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        float2 h = carry;
+        if (cl > 1 && ok) {
+            float4 m = ex.group_map[0][lane];
+            bool rst = RESET && ex.group_rst[0];
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                g[w] = ex.group_map[w][lane];
-                if (RESET && ex.group_rst[w]) rst |= 1u << w;
+            for (int w = 1; w < NW; ++w) {
+                const float4 g = ex.group_map[w][lane];
+                const bool gr = RESET && ex.group_rst[w];
+                const float2 hh = apply(g, gr, make_float2(m.z, m.w));
+                const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g.x, g.y), make_float2(m.x, m.y));
+                m = make_float4(aa.x, aa.y, hh.x, hh.y);
+                rst |= gr;
             }
-            float2 h = carry;
-            if (cl > 1 && ok) {
-                float4 m = g[0];
-#pragma unroll
-                for (int w = 1; w < NW; ++w) {
-                    const bool gr = RESET && ((rst >> w) & 1);
-                    const float2 hh = apply(g[w], gr, make_float2(m.z, m.w));
-                    const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g[w].x, g[w].y), make_float2(m.x, m.y));
-                    m = make_float4(aa.x, aa.y, hh.x, hh.y);
-                }
-                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
-                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
-                __syncwarp();
-                if (!(rank == 0 && it == withhold)) {
-                    for (int to = 0; to < cl; ++to)
-                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
-                    if (RESET && lane < cl)
-                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
-                }
-                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
-                for (int q = 0; q < cl; ++q) {
-                    if (q == rank) h = carry;
-                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                ex.entering[w][lane] = h;
-                h = apply(g[w], RESET && ((rst >> w) & 1), h);
-            }
-            if (cl == 1) carry = h;
+            const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+            if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
-        }
-        if (p.final_state && active && rank == 0)
-            *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
-    } else {
-        int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
-        const int64_t nst = (L + kInterval - 1) / kInterval;
-        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
-        // lane 0 loads round n's tiles into their slot: x and gate_x, which
-        // arms the slot's barrier for all three, and gate_a, whose place holds y
-        // until its store has read it
-        auto load_x = [&](int n) {
-            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-            const int t = static_cast<int>(t0 + n * round);
-            tc::mbar_expect_tx(bar, 3 * TB);
-            tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-        };
-        auto load_a = [&](int n) {
-            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
-                              static_cast<int>(t0 + n * round), static_cast<int>(b));
-        };
-        if (lane == 0) {
-            for (int n = 0; n < ST && n < rounds; ++n) {
-                load_x(n);
-                load_a(n);
+            if (!(rank == 0 && it == withhold)) {
+                for (int to = 0; to < cl; ++to)
+                    store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
+                if (RESET && lane < cl)
+                    store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
+            }
+            ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+            for (int q = 0; q < cl; ++q) {
+                if (q == rank) h = carry;
+                carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
             }
         }
-        const float2 k = decay_rates(p, c, active);
-        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-        const int64_t first = t0;
-        bool ok = true;
-        bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
-        for (int it = 0; it < rounds; ++it) {
-            const int64_t t = first + it * round;
-            const int slot = it % ST;
-            const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
-            uint32_t rst = 0;
-            if constexpr (RESET) {
-                rst = __ballot_sync(0xffffffffu, flag);
-                flag = reset_flag(p.reset, b, t + round, L, lane);
-            }
-            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
-            // the gates and the group's map
-            float2 em1[TPT], u[TPT];
 #pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                const uint8_t* row = src + j * kRowBytes<T>;
-                float2 r, i, a;
-                sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
-                              read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
-                decays<EXACT>(mul2(k, r), slow, em1[j], a);
-                float2 n = input_weight(em1[j]);
-                if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
-                u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
-            }
-            __syncwarp();
-            if (lane == 0) {
-                if (ST == 2 && it > 0 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();  // the previous round's y has left
-                    load_a(it + 1);
-                }
-                if (it + ST < rounds) load_x(it + ST);
-            }
-            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-            if (left < TPT) {  // tokens past the end change nothing
-#pragma unroll
-                for (int j = 0; j < TPT; ++j)
-                    if (j >= left) em1[j] = u[j] = dup(0.0f);
-            }
-            float2 A = dup(1.0f), H = dup(0.0f);
-#pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                if (RESET && ((rst >> j) & 1)) {
-                    A = dup(0.0f);
-                    H = u[j];
-                } else {
-                    A = fma2(em1[j], A, A);
-                    H = add2(H, fma2(em1[j], H, u[j]));
-                }
-            }
-            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-            // the outputs, over gate_a's tile, and out
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
-            float2 h = ex.entering[warp][lane];
-            // a tile starts at a multiple of the interval: group 0 keeps its state
-            if (warp == 0 && p.states && active && left > 0)
-                *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
-#pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                if (RESET && ((rst >> j) & 1)) h = u[j];
-                else h = add2(h, fma2(em1[j], h, u[j]));
-                *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
-            }
-            tc::fence_smem_async();
-            __syncwarp();
-            if (lane == 0) {
-                if (left > 0) {
-                    tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
-                                       static_cast<int>(t), static_cast<int>(b));
-                    tc::bulk_commit_group();
-                }
-                if (ST == 1 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();
-                    load_a(it + 1);
-                }
-            }
+        for (int w = 0; w < NW; ++w) {
+            ex.entering[w][lane] = h;
+            h = apply(ex.group_map[w][lane], RESET && ex.group_rst[w], h);
         }
-        if (lane == 0) tc::bulk_wait_all();
+        if (cl == 1) carry = h;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+        return ok;
+    };
+    int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
+    const int64_t nst = (L + kInterval - 1) / kInterval;
+    const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
+    // lane 0 loads round n's tiles into their slot: x and gate_x, which
+    // arms the slot's barrier for all three, and gate_a, whose place holds y
+    // until its store has read it
+    auto load_x = [&](int n) {
+        const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+        const int t = static_cast<int>(t0 + n * round);
+        tc::mbar_expect_tx(bar, 3 * TB);
+        tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+        tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+    };
+    auto load_a = [&](int n) {
+        const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+        tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
+                          static_cast<int>(t0 + n * round), static_cast<int>(b));
+    };
+    if (lane == 0) {
+        for (int n = 0; n < ST && n < rounds; ++n) {
+            load_x(n);
+            load_a(n);
+        }
     }
+    const float2 k = decay_rates(p, c, active);
+    const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+    const int64_t first = t0;
+    bool ok = true;
+    bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
+    for (int it = 0; it < rounds; ++it) {
+        const int64_t t = first + it * round;
+        const int slot = it % ST;
+        const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
+        uint32_t rst = 0;
+        if constexpr (RESET) {
+            rst = __ballot_sync(0xffffffffu, flag);
+            flag = reset_flag(p.reset, b, t + round, L, lane);
+        }
+        if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+        // the gates and the group's map
+        float2 em1[TPT], u[TPT];
+#pragma unroll
+        for (int j = 0; j < TPT; ++j) {
+            const uint8_t* row = src + j * kRowBytes<T>;
+            float2 r, i, a;
+            sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
+                          read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
+            decays<EXACT>(mul2(k, r), slow, em1[j], a);
+            float2 n = input_weight(em1[j]);
+            if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
+            u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (ST == 2 && it > 0 && it + 1 < rounds) {
+                tc::bulk_wait_read_all();  // the previous round's y has left
+                load_a(it + 1);
+            }
+            if (it + ST < rounds) load_x(it + ST);
+        }
+        const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
+        if (left < TPT) {  // tokens past the end change nothing
+#pragma unroll
+            for (int j = 0; j < TPT; ++j)
+                if (j >= left) em1[j] = u[j] = dup(0.0f);
+        }
+        float2 A = dup(1.0f), H = dup(0.0f);
+#pragma unroll
+        for (int j = 0; j < TPT; ++j) {
+            if (RESET && ((rst >> j) & 1)) {
+                A = dup(0.0f);
+                H = u[j];
+            } else {
+                A = fma2(em1[j], A, A);
+                H = add2(H, fma2(em1[j], H, u[j]));
+            }
+        }
+        ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+        if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+        // the outputs, over gate_a's tile, and out
+        if (warp == 0) ok = hand_out(it, ok);
+        else if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+        float2 h = ex.entering[warp][lane];
+        // a tile starts at a multiple of the interval: group 0 keeps its state
+        if (warp == 0 && p.states && active && left > 0)
+            *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
+#pragma unroll
+        for (int j = 0; j < TPT; ++j) {
+            if (RESET && ((rst >> j) & 1)) h = u[j];
+            else h = add2(h, fma2(em1[j], h, u[j]));
+            *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
+        }
+        tc::fence_smem_async();
+        __syncwarp();
+        if (lane == 0) {
+            if (left > 0) {
+                tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
+                                   static_cast<int>(t), static_cast<int>(b));
+                tc::bulk_commit_group();
+            }
+            if (ST == 1 && it + 1 < rounds) {
+                tc::bulk_wait_read_all();
+                load_a(it + 1);
+            }
+        }
+    }
+    if (lane == 0) tc::bulk_wait_all();
+    if (p.final_state && active && rank == 0 && warp == 0)
+        *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
     if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
@@ -443,9 +439,9 @@ __global__ void __launch_bounds__(TPB, 3)
 // The gradient, the same way from the last token to the first: a group also has
 // the map of the adjoint it passes on, c <- a (dy + c) token by token backwards,
 // whose factor is the same A.  The state entering a tile is the forward's (a
-// tile is one interval), so only the adjoint crosses tiles.  The 8 warps form
-// both maps, the ninth hands each group its entering state and adjoint, and
-// the group is replayed, forwards for the states and backwards for the
+// tile is one interval), so only the adjoint crosses tiles.  The warps form
+// both maps, warp 0 hands each group its entering state and adjoint, and the
+// group is replayed, forwards for the states and backwards for the
 // outputs, which take the places of x, gate_x and gate_a in shared memory.
 struct ExchangeBwd {
     float4 group_map[NW][32];             // A, H
@@ -495,200 +491,199 @@ __global__ void __launch_bounds__(TPB, 2)
     if (cl > 1) cluster_sync_all();
     float2 sum = dup(0.0f);
 
-    if (warp == NW) {
-        const int64_t nst = (L + kInterval - 1) / kInterval;
-        // the kept state entering this CTA's tile of a round (rounds run backwards)
-        auto kept = [&](int it) {
-            const int64_t tile = static_cast<int64_t>(rounds - 1 - it) * cl + rank;
-            return active && it < rounds && tile < nst
-                       ? *reinterpret_cast<const float2*>(p.states + (b * nst + tile) * C + c)
-                       : dup(0.0f);
-        };
-        float2 carry = (active && p.d_final) ? *reinterpret_cast<const float2*>(p.d_final + b * C + c) : dup(0.0f);
-        float2 next = kept(0);
-        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
-        bool ok = true;
-        for (int it = 0; it < rounds; ++it) {
-            const int buf = it & 1;
-            float2 h = next;
-            next = kept(it + 1);
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
-            ok = __all_sync(0xffffffffu, ok);
-            float2 A[NW], G[NW];
-            uint32_t rst = 0;
+    // warp 0's part in a round, as in the forward
+    const int64_t nst = (L + kInterval - 1) / kInterval;
+    // the kept state entering this CTA's tile of a round (rounds run backwards)
+    auto kept = [&](int it) {
+        const int64_t tile = static_cast<int64_t>(rounds - 1 - it) * cl + rank;
+        return warp == 0 && active && it < rounds && tile < nst
+                   ? *reinterpret_cast<const float2*>(p.states + (b * nst + tile) * C + c)
+                   : dup(0.0f);
+    };
+    float2 carry = (warp == 0 && active && p.d_final) ? *reinterpret_cast<const float2*>(p.d_final + b * C + c) : dup(0.0f);
+    float2 next = kept(0);
+    const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+    auto hand_out = [&](int it, bool ok) {
+        const int buf = it & 1;
+        float2 h = next;
+        next = kept(it + 1);
+        if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+        ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float4 g = ex.group_map[w][lane];
-                A[w] = make_float2(g.x, g.y);
-                G[w] = ex.group_rev[w][lane];
-                if (RESET && ex.group_rst[w]) rst |= 1u << w;
-                *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
-                h = apply(g, RESET && ((rst >> w) & 1), h);
-            }
-            auto step = [&](int w, float2 v) { return RESET && ((rst >> w) & 1) ? G[w] : fma2(A[w], v, G[w]); };
-            float2 cin = carry;
-            if (cl > 1 && ok) {
-                float2 a = A[NW - 1], g = G[NW - 1];
-#pragma unroll
-                for (int w = NW - 2; w >= 0; --w) {
-                    g = step(w, g);
-                    a = RESET && ((rst >> w) & 1) ? dup(0.0f) : mul2(A[w], a);
-                }
-                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
-                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
-                __syncwarp();
-                if (!(rank == 0 && it == withhold)) {
-                    for (int to = 0; to < cl; ++to)
-                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), make_float4(a.x, a.y, g.x, g.y),
-                                    in_rank(&ex.tiles_ready[buf], to));
-                    if (RESET && lane < cl)
-                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
-                }
-                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
-                for (int q = cl - 1; q >= 0; --q) {
-                    if (q == rank) cin = carry;
-                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
-                }
-            }
-#pragma unroll
-            for (int w = NW - 1; w >= 0; --w) {
-                *(reinterpret_cast<float2*>(&ex.entering[w][lane]) + 1) = cin;
-                cin = step(w, cin);
-            }
-            if (cl == 1) carry = cin;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+        for (int w = 0; w < NW; ++w) {
+            *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
+            h = apply(ex.group_map[w][lane], RESET && ex.group_rst[w], h);
         }
-        if (p.d_init && active && rank == 0) *reinterpret_cast<float2*>(p.d_init + b * C + c) = carry;
-    } else {
-        const int64_t first = static_cast<int64_t>(rank) * TILE + warp * TPT;
-        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 4 * TB;
-        const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
-        auto token = [&](int it) { return first + static_cast<int64_t>(rounds - 1 - it) * round; };
-        auto load = [&](int n) {
-            const uint32_t dst = tiles + (n % ST) * 4 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-            const int t = static_cast<int>(token(n));
-            tc::mbar_expect_tx(bar, 4 * TB);
-            tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
-            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, ci, t, bi);
-            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, ci, t, bi);
-            tc::tma_load_rows(dst + 3 * TB, &maps.dy, bar, ci, t, bi);
+        auto factor = [&](int w) { return *reinterpret_cast<const float2*>(&ex.group_map[w][lane]); };
+        auto step = [&](int w, float2 v) {
+            const float2 G = ex.group_rev[w][lane];
+            return RESET && ex.group_rst[w] ? G : fma2(factor(w), v, G);
         };
-        if (lane == 0)
-            for (int n = 0; n < ST && n < rounds; ++n) load(n);
-        const float2 k = decay_rates(p, c, active);
-        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-        bool ok = true;
-        bool flag = RESET && reset_flag(p.reset, b, token(0), L, lane);
-        for (int it = 0; it < rounds; ++it) {
-            const int64_t t = token(it);
-            const int slot = it % ST;
-            uint8_t* src = ring + (warp * ST + slot) * 4 * TB + lane * sizeof(Raw);
-            auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * TB + j * kRowBytes<T>); };
-            uint32_t rst = 0;
-            if constexpr (RESET) {
-                rst = __ballot_sync(0xffffffffu, flag);
-                flag = it + 1 < rounds && reset_flag(p.reset, b, t - round, L, lane);
-            }
-            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
-            float2 r[TPT], i[TPT], em1[TPT];
-            float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
+        float2 cin = carry;
+        if (cl > 1 && ok) {
+            float2 a = factor(NW - 1), g = ex.group_rev[NW - 1][lane];
+            bool rst = RESET && ex.group_rst[NW - 1];
 #pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                float2 a;
-                sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
-                decays<EXACT>(mul2(k, r[j]), slow, em1[j], a);
-                float2 n = input_weight(em1[j]);
-                const bool rs = RESET && ((rst >> j) & 1);
-                if (rs) n = dup(1.0f);
-                float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
-                if (rs) {
-                    A = dup(0.0f);
-                    H = u;
-                } else {
-                    A = fma2(em1[j], A, A);
-                    H = add2(H, fma2(em1[j], H, u));
-                }
+            for (int w = NW - 2; w >= 0; --w) {
+                g = step(w, g);
+                a = RESET && ex.group_rst[w] ? dup(0.0f) : mul2(factor(w), a);
+                rst |= RESET && ex.group_rst[w];
             }
-#pragma unroll
-            for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
-                G = add2(G, Pair<T>::widen(*at(3, j)));
-                G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
-            }
-            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-            ex.group_rev[warp][lane] = G;
-            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+            const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+            if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
             __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-                if (ST == 2 && it > 0 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();  // the previous round's outputs have left
-                    load(it + 1);
-                }
+            if (!(rank == 0 && it == withhold)) {
+                for (int to = 0; to < cl; ++to)
+                    store_async(in_rank(&ex.tile_map[buf][rank][lane], to), make_float4(a.x, a.y, g.x, g.y),
+                                in_rank(&ex.tiles_ready[buf], to));
+                if (RESET && lane < cl)
+                    store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
             }
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
-            const float4 in = ex.entering[warp][lane];
-            float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
-            float2 hp[TPT];
-#pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                hp[j] = h;
-                const bool rs = RESET && ((rst >> j) & 1);
-                const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
-                const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                h = rs ? u : add2(h, fma2(em1[j], h, u));
-            }
-#pragma unroll
-            for (int j = TPT - 1; j >= 0; --j) {
-                const bool rs = RESET && ((rst >> j) & 1);
-                const float2 x = Pair<T>::widen(*at(0, j));
-                g = add2(g, Pair<T>::widen(*at(3, j)));
-                const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
-                float2 a = add2(em1[j], dup(1.0f));
-                if (!slow) {  // a small decay as it is, not as 1 + em1
-                    const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-                    if (!(la.x >= -0.25f)) a.x = e.x;
-                    if (!(la.y >= -0.25f)) a.y = e.y;
-                }
-                // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
-                // gives a finite dla, times la = 0
-                const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
-                const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
-                const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
-                const float2 dx = mul2(mul2(g, n), i[j]);
-                const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
-                float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
-                if (rs) dla = dup(0.0f);
-                const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
-                if (j < left) sum = fma2(dla, r[j], sum);
-                g = rs ? dup(0.0f) : fma2(em1[j], g, g);
-                *at(0, j) = Pair<T>::narrow(dx);
-                *at(1, j) = Pair<T>::narrow(dgx);
-                *at(2, j) = Pair<T>::narrow(dga);
-            }
-            tc::fence_smem_async();
-            __syncwarp();
-            if (lane == 0) {
-                if (left > 0) {
-                    const uint32_t out = tiles + slot * 4 * TB;
-                    tc::tma_store_rows(&maps.dx, out, ci, static_cast<int>(t), bi);
-                    tc::tma_store_rows(&maps.dgate_x, out + TB, ci, static_cast<int>(t), bi);
-                    tc::tma_store_rows(&maps.dgate_a, out + 2 * TB, ci, static_cast<int>(t), bi);
-                    tc::bulk_commit_group();
-                }
-                if (ST == 1 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();
-                    load(it + 1);
-                }
+            ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+            for (int q = cl - 1; q >= 0; --q) {
+                if (q == rank) cin = carry;
+                carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
             }
         }
-        if (lane == 0) tc::bulk_wait_all();
+#pragma unroll
+        for (int w = NW - 1; w >= 0; --w) {
+            *(reinterpret_cast<float2*>(&ex.entering[w][lane]) + 1) = cin;
+            cin = step(w, cin);
+        }
+        if (cl == 1) carry = cin;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+        return ok;
+    };
+    const int64_t first = static_cast<int64_t>(rank) * TILE + warp * TPT;
+    const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 4 * TB;
+    const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
+    auto token = [&](int it) { return first + static_cast<int64_t>(rounds - 1 - it) * round; };
+    auto load = [&](int n) {
+        const uint32_t dst = tiles + (n % ST) * 4 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+        const int t = static_cast<int>(token(n));
+        tc::mbar_expect_tx(bar, 4 * TB);
+        tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
+        tc::tma_load_rows(dst + TB, &maps.gate_x, bar, ci, t, bi);
+        tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, ci, t, bi);
+        tc::tma_load_rows(dst + 3 * TB, &maps.dy, bar, ci, t, bi);
+    };
+    if (lane == 0)
+        for (int n = 0; n < ST && n < rounds; ++n) load(n);
+    const float2 k = decay_rates(p, c, active);
+    const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+    bool ok = true;
+    bool flag = RESET && reset_flag(p.reset, b, token(0), L, lane);
+    for (int it = 0; it < rounds; ++it) {
+        const int64_t t = token(it);
+        const int slot = it % ST;
+        uint8_t* src = ring + (warp * ST + slot) * 4 * TB + lane * sizeof(Raw);
+        auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * TB + j * kRowBytes<T>); };
+        uint32_t rst = 0;
+        if constexpr (RESET) {
+            rst = __ballot_sync(0xffffffffu, flag);
+            flag = it + 1 < rounds && reset_flag(p.reset, b, t - round, L, lane);
+        }
+        const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
+        if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+        float2 r[TPT], i[TPT], em1[TPT];
+        float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
+#pragma unroll
+        for (int j = 0; j < TPT; ++j) {
+            float2 a;
+            sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
+            decays<EXACT>(mul2(k, r[j]), slow, em1[j], a);
+            float2 n = input_weight(em1[j]);
+            const bool rs = RESET && ((rst >> j) & 1);
+            if (rs) n = dup(1.0f);
+            float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+            if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
+            if (rs) {
+                A = dup(0.0f);
+                H = u;
+            } else {
+                A = fma2(em1[j], A, A);
+                H = add2(H, fma2(em1[j], H, u));
+            }
+        }
+#pragma unroll
+        for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
+            G = add2(G, Pair<T>::widen(*at(3, j)));
+            G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
+        }
+        ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+        ex.group_rev[warp][lane] = G;
+        if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+            if (ST == 2 && it > 0 && it + 1 < rounds) {
+                tc::bulk_wait_read_all();  // the previous round's outputs have left
+                load(it + 1);
+            }
+        }
+        if (warp == 0) ok = hand_out(it, ok);
+        else if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+        const float4 in = ex.entering[warp][lane];
+        float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
+        float2 hp[TPT];
+#pragma unroll
+        for (int j = 0; j < TPT; ++j) {
+            hp[j] = h;
+            const bool rs = RESET && ((rst >> j) & 1);
+            const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
+            const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+            h = rs ? u : add2(h, fma2(em1[j], h, u));
+        }
+#pragma unroll
+        for (int j = TPT - 1; j >= 0; --j) {
+            const bool rs = RESET && ((rst >> j) & 1);
+            const float2 x = Pair<T>::widen(*at(0, j));
+            g = add2(g, Pair<T>::widen(*at(3, j)));
+            const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
+            float2 a = add2(em1[j], dup(1.0f));
+            if (!slow) {  // a small decay as it is, not as 1 + em1
+                const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
+                if (!(la.x >= -0.25f)) a.x = e.x;
+                if (!(la.y >= -0.25f)) a.y = e.y;
+            }
+            // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
+            // gives a finite dla, times la = 0
+            const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
+            const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
+            const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
+            const float2 dx = mul2(mul2(g, n), i[j]);
+            const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
+            float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
+            if (rs) dla = dup(0.0f);
+            const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
+            if (j < left) sum = fma2(dla, r[j], sum);
+            g = rs ? dup(0.0f) : fma2(em1[j], g, g);
+            *at(0, j) = Pair<T>::narrow(dx);
+            *at(1, j) = Pair<T>::narrow(dgx);
+            *at(2, j) = Pair<T>::narrow(dga);
+        }
+        tc::fence_smem_async();
+        __syncwarp();
+        if (lane == 0) {
+            if (left > 0) {
+                const uint32_t out = tiles + slot * 4 * TB;
+                tc::tma_store_rows(&maps.dx, out, ci, static_cast<int>(t), bi);
+                tc::tma_store_rows(&maps.dgate_x, out + TB, ci, static_cast<int>(t), bi);
+                tc::tma_store_rows(&maps.dgate_a, out + 2 * TB, ci, static_cast<int>(t), bi);
+                tc::bulk_commit_group();
+            }
+            if (ST == 1 && it + 1 < rounds) {
+                tc::bulk_wait_read_all();
+                load(it + 1);
+            }
+        }
     }
+    if (lane == 0) tc::bulk_wait_all();
+    if (p.d_init && active && rank == 0 && warp == 0) *reinterpret_cast<float2*>(p.d_init + b * C + c) = carry;
     // the CTA's sums of dla r, group after group
     __syncthreads();
-    if (warp < NW) *reinterpret_cast<float2*>(&ex.entering[warp][lane]) = sum;
+    *reinterpret_cast<float2*>(&ex.entering[warp][lane]) = sum;
     __syncthreads();
     if (warp == 0 && active) {
         float2 s = dup(0.0f);
