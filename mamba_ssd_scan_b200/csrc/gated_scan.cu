@@ -9,18 +9,18 @@
 // registers, while the gates (about 4 special-function results per element)
 // are formed once and the inputs are read once.
 //
-// A warp takes one group of tokens of 64 channels (a pair per lane); the 8
-// warps of a CTA take consecutive groups (a tile of 64 tokens), and the CTAs of
-// a cluster consecutive tiles.  Warp 0 composes the tile's map, sends it to the
-// cluster's CTAs through distributed shared memory (asynchronous stores that
-// complete on the receiver's mbarrier), and hands each group its entering
-// state.  The order of composition is fixed, so
+// A compute warp takes one group of tokens of 64 channels (a pair per lane);
+// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens),
+// and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
+// tile's map, sends it to the cluster's CTAs through distributed shared memory
+// (asynchronous stores that complete on the receiver's mbarrier), and hands
+// each group its entering state.  The order of composition is fixed, so
 // results do not depend on timing; there is no workspace and no wait on another
 // cluster.  Every mbarrier wait is bounded: on expiry the CTA raises its abort
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
-#include <stdlib.h>
+#include <atomic>
+#include <type_traits>
 #include <utility>
-
 #include "mixers.h"
 #include "tcgen05.cuh"
 #include "rows_tma.cuh"
@@ -30,8 +30,9 @@ namespace ssd {
 namespace {
 
 constexpr int kInterval = SSD_GATED_SCAN_INTERVAL;
-constexpr int NW = 8;            // warps (groups) per CTA
-constexpr int TPB = NW * 32;
+constexpr int NW = 8;                   // groups per CTA, a warp each
+constexpr int kFwdThreads = (NW + 1) * 32;  // and the warp that composes their maps
+constexpr int kBwdThreads = NW * 32;
 constexpr int TPT = 8;           // tokens per group
 constexpr int TILE = NW * TPT;   // tokens per CTA and round
 static_assert(TILE == kInterval, "a tile starts where a state is kept");
@@ -130,10 +131,12 @@ __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& 
 // 1 - a^2 = -em1 (2 + em1) without cancellation.  Down to -1/4 from the Taylor
 // series to the sixth power (what it leaves out is below 2^-24 of em1), beyond
 // from e^la.  la never falls below the channel's own -scale softplus(decay),
-// so where that is above -1/4 (`slow`, the same for a whole warp; the usual
-// decays of 0.9 to 0.999 at the open gate) the second form is not evaluated.
-template <bool EXACT>
-__device__ __forceinline__ void decays(float2 la, bool slow, float2& em1, float2& a) {
+// so where that is above -1/4 (SLOW; the usual decays of 0.9 to 0.999 at the
+// open gate) the second form is not evaluated.  The choice is made once per
+// group, not per token: a branch between the tokens kept them from overlapping
+// (220 cycles per token and warp).
+template <bool EXACT, bool SLOW>
+__device__ __forceinline__ void decays(float2 la, float2& em1, float2& a) {
     float2 q = dup(1.0f / 720.0f);
     q = fma2(q, la, dup(1.0f / 120.0f));
     q = fma2(q, la, dup(1.0f / 24.0f));
@@ -141,16 +144,11 @@ __device__ __forceinline__ void decays(float2 la, bool slow, float2& em1, float2
     q = fma2(q, la, dup(0.5f));
     em1 = fma2(mul2(q, la), la, la);
     a = add2(em1, dup(1.0f));
-    if (!slow) {
+    if constexpr (!SLOW) {
         const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-        if (!(la.x >= -0.25f)) {
-            a.x = e.x;
-            em1.x = e.x - 1.0f;
-        }
-        if (!(la.y >= -0.25f)) {
-            a.y = e.y;
-            em1.y = e.y - 1.0f;
-        }
+        const bool nx = la.x >= -0.25f, ny = la.y >= -0.25f;
+        a = make_float2(nx ? a.x : e.x, ny ? a.y : e.y);
+        em1 = make_float2(nx ? em1.x : e.x - 1.0f, ny ? em1.y : e.y - 1.0f);
     }
 }
 // sqrt(1 - a^2)
@@ -243,7 +241,7 @@ struct ScanMaps {
 };
 
 template <typename T, bool RESET>
-__global__ void __launch_bounds__(TPB, 3)
+__global__ void __launch_bounds__(kFwdThreads, 3)
     gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
     constexpr int ST = kStages<T>, TB = kTileBytes<T>;
@@ -273,164 +271,172 @@ __global__ void __launch_bounds__(TPB, 3)
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // every CTA's barriers exist before a peer completes on them
 
-    // warp 0's part in a round (false once a wait has given up: no map is then
-    // sent, received or waited for)
-    float2 carry = (warp == 0 && active && p.init_state)
-                       ? *reinterpret_cast<const float2*>(p.init_state + b * C + c) : dup(0.0f);
-    const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
-    auto hand_out = [&](int it, bool ok) {
-        const int buf = it & 1;
-        if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
-        ok = __all_sync(0xffffffffu, ok);
-        float2 h = carry;
-        if (cl > 1 && ok) {
-            float4 m = ex.group_map[0][lane];
-            bool rst = RESET && ex.group_rst[0];
+    if (warp == NW) {
+        float2 carry = (active && p.init_state) ? *reinterpret_cast<const float2*>(p.init_state + b * C + c)
+                                                : dup(0.0f);
+        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+        bool ok = true;  // (whole-warp: no map is sent, received or waited for after a timeout)
+        for (int it = 0; it < rounds; ++it) {
+            const int buf = it & 1;
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            float4 g[NW];
+            uint32_t rst = 0;
 #pragma unroll
-            for (int w = 1; w < NW; ++w) {
-                const float4 g = ex.group_map[w][lane];
-                const bool gr = RESET && ex.group_rst[w];
-                const float2 hh = apply(g, gr, make_float2(m.z, m.w));
-                const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g.x, g.y), make_float2(m.x, m.y));
-                m = make_float4(aa.x, aa.y, hh.x, hh.y);
-                rst |= gr;
+            for (int w = 0; w < NW; ++w) {
+                g[w] = ex.group_map[w][lane];
+                if (RESET && ex.group_rst[w]) rst |= 1u << w;
             }
-            const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
-            if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+            float2 h = carry;
+            if (cl > 1 && ok) {
+                float4 m = g[0];
+#pragma unroll
+                for (int w = 1; w < NW; ++w) {
+                    const bool gr = RESET && ((rst >> w) & 1);
+                    const float2 hh = apply(g[w], gr, make_float2(m.z, m.w));
+                    const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g[w].x, g[w].y), make_float2(m.x, m.y));
+                    m = make_float4(aa.x, aa.y, hh.x, hh.y);
+                }
+                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+                __syncwarp();
+                if (!(rank == 0 && it == withhold)) {
+                    for (int to = 0; to < cl; ++to)
+                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
+                    if (RESET && lane < cl)
+                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
+                }
+                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+                for (int q = 0; q < cl; ++q) {
+                    if (q == rank) h = carry;
+                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                ex.entering[w][lane] = h;
+                h = apply(g[w], RESET && ((rst >> w) & 1), h);
+            }
+            if (cl == 1) carry = h;
             __syncwarp();
-            if (!(rank == 0 && it == withhold)) {
-                for (int to = 0; to < cl; ++to)
-                    store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
-                if (RESET && lane < cl)
-                    store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
-            }
-            ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
-            for (int q = 0; q < cl; ++q) {
-                if (q == rank) h = carry;
-                carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
-            }
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
         }
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            ex.entering[w][lane] = h;
-            h = apply(ex.group_map[w][lane], RESET && ex.group_rst[w], h);
-        }
-        if (cl == 1) carry = h;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
-        return ok;
-    };
-    int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
-    const int64_t nst = (L + kInterval - 1) / kInterval;
-    const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
-    // lane 0 loads round n's tiles into their slot: x and gate_x, which
-    // arms the slot's barrier for all three, and gate_a, whose place holds y
-    // until its store has read it
-    auto load_x = [&](int n) {
-        const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-        const int t = static_cast<int>(t0 + n * round);
-        tc::mbar_expect_tx(bar, 3 * TB);
-        tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-        tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-    };
-    auto load_a = [&](int n) {
-        const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-        tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
-                          static_cast<int>(t0 + n * round), static_cast<int>(b));
-    };
-    if (lane == 0) {
-        for (int n = 0; n < ST && n < rounds; ++n) {
-            load_x(n);
-            load_a(n);
-        }
-    }
-    const float2 k = decay_rates(p, c, active);
-    const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-    const int64_t first = t0;
-    bool ok = true;
-    bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
-    for (int it = 0; it < rounds; ++it) {
-        const int64_t t = first + it * round;
-        const int slot = it % ST;
-        const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
-        uint32_t rst = 0;
-        if constexpr (RESET) {
-            rst = __ballot_sync(0xffffffffu, flag);
-            flag = reset_flag(p.reset, b, t + round, L, lane);
-        }
-        if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
-        // the gates and the group's map
-        float2 em1[TPT], u[TPT];
-#pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            const uint8_t* row = src + j * kRowBytes<T>;
-            float2 r, i, a;
-            sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
-                          read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
-            decays<EXACT>(mul2(k, r), slow, em1[j], a);
-            float2 n = input_weight(em1[j]);
-            if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
-            u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
-        }
-        __syncwarp();
+        if (p.final_state && active && rank == 0)
+            *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
+    } else {
+        int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
+        const int64_t nst = (L + kInterval - 1) / kInterval;
+        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
+        // lane 0 loads round n's tiles into their slot: x and gate_x, which
+        // arms the slot's barrier for all three, and gate_a, whose place holds y
+        // until its store has read it
+        auto load_x = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+            const int t = static_cast<int>(t0 + n * round);
+            tc::mbar_expect_tx(bar, 3 * TB);
+            tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+        };
+        auto load_a = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
+            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
+                              static_cast<int>(t0 + n * round), static_cast<int>(b));
+        };
         if (lane == 0) {
-            if (ST == 2 && it > 0 && it + 1 < rounds) {
-                tc::bulk_wait_read_all();  // the previous round's y has left
-                load_a(it + 1);
+            for (int n = 0; n < ST && n < rounds; ++n) {
+                load_x(n);
+                load_a(n);
             }
-            if (it + ST < rounds) load_x(it + ST);
         }
-        const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-        if (left < TPT) {  // tokens past the end change nothing
+        const float2 k = decay_rates(p, c, active);
+        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+        const int64_t first = t0;
+        bool ok = true;
+        bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
+        for (int it = 0; it < rounds; ++it) {
+            const int64_t t = first + it * round;
+            const int slot = it % ST;
+            const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
+            uint32_t rst = 0;
+            if constexpr (RESET) {
+                rst = __ballot_sync(0xffffffffu, flag);
+                flag = reset_flag(p.reset, b, t + round, L, lane);
+            }
+            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+            // the gates and the group's map
+            float2 em1[TPT], u[TPT];
+            auto form = [&](auto is_slow) {
 #pragma unroll
-            for (int j = 0; j < TPT; ++j)
-                if (j >= left) em1[j] = u[j] = dup(0.0f);
-        }
-        float2 A = dup(1.0f), H = dup(0.0f);
+                for (int j = 0; j < TPT; ++j) {
+                    const uint8_t* row = src + j * kRowBytes<T>;
+                    float2 r, i, a;
+                    sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
+                                  read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
+                    decays<EXACT, decltype(is_slow)::value>(mul2(k, r), em1[j], a);
+                    float2 n = input_weight(em1[j]);
+                    if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
+                    u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
+                }
+            };
+            if (slow) form(std::true_type());
+            else form(std::false_type());
+            __syncwarp();
+            if (lane == 0) {
+                if (ST == 2 && it > 0 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();  // the previous round's y has left
+                    load_a(it + 1);
+                }
+                if (it + ST < rounds) load_x(it + ST);
+            }
+            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
+            if (left < TPT) {  // tokens past the end change nothing
 #pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            if (RESET && ((rst >> j) & 1)) {
-                A = dup(0.0f);
-                H = u[j];
-            } else {
-                A = fma2(em1[j], A, A);
-                H = add2(H, fma2(em1[j], H, u[j]));
+                for (int j = 0; j < TPT; ++j)
+                    if (j >= left) em1[j] = u[j] = dup(0.0f);
             }
-        }
-        ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-        // the outputs, over gate_a's tile, and out
-        if (warp == 0) ok = hand_out(it, ok);
-        else if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
-        float2 h = ex.entering[warp][lane];
-        // a tile starts at a multiple of the interval: group 0 keeps its state
-        if (warp == 0 && p.states && active && left > 0)
-            *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
+            float2 A = dup(1.0f), H = dup(0.0f);
 #pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            if (RESET && ((rst >> j) & 1)) h = u[j];
-            else h = add2(h, fma2(em1[j], h, u[j]));
-            *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
-        }
-        tc::fence_smem_async();
-        __syncwarp();
-        if (lane == 0) {
-            if (left > 0) {
-                tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
-                                   static_cast<int>(t), static_cast<int>(b));
-                tc::bulk_commit_group();
+            for (int j = 0; j < TPT; ++j) {
+                if (RESET && ((rst >> j) & 1)) {
+                    A = dup(0.0f);
+                    H = u[j];
+                } else {
+                    A = fma2(em1[j], A, A);
+                    H = add2(H, fma2(em1[j], H, u[j]));
+                }
             }
-            if (ST == 1 && it + 1 < rounds) {
-                tc::bulk_wait_read_all();
-                load_a(it + 1);
+            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+            // the outputs, over gate_a's tile, and out
+            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+            float2 h = ex.entering[warp][lane];
+            // a tile starts at a multiple of the interval: group 0 keeps its state
+            if (warp == 0 && p.states && active && left > 0)
+                *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                if (RESET && ((rst >> j) & 1)) h = u[j];
+                else h = add2(h, fma2(em1[j], h, u[j]));
+                *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
+            }
+            tc::fence_smem_async();
+            __syncwarp();
+            if (lane == 0) {
+                if (left > 0) {
+                    tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
+                                       static_cast<int>(t), static_cast<int>(b));
+                    tc::bulk_commit_group();
+                }
+                if (ST == 1 && it + 1 < rounds) {
+                    tc::bulk_wait_read_all();
+                    load_a(it + 1);
+                }
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
     }
-    if (lane == 0) tc::bulk_wait_all();
-    if (p.final_state && active && rank == 0 && warp == 0)
-        *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
     if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
@@ -460,7 +466,7 @@ struct ScanBwdMaps {
 };
 
 template <typename T, bool RESET>
-__global__ void __launch_bounds__(TPB, 2)
+__global__ void __launch_bounds__(kBwdThreads, 2)
     gated_scan_bwd_kernel(GatedScanParams p, const __grid_constant__ ScanBwdMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
     constexpr int ST = kStagesBwd<T>, TB = kTileBytes<T>;
@@ -588,11 +594,18 @@ __global__ void __launch_bounds__(TPB, 2)
         if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
         float2 r[TPT], i[TPT], em1[TPT];
         float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
+        auto form = [&](auto is_slow) {
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                float2 a;
+                sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
+                decays<EXACT, decltype(is_slow)::value>(mul2(k, r[j]), em1[j], a);
+            }
+        };
+        if (slow) form(std::true_type());
+        else form(std::false_type());
 #pragma unroll
         for (int j = 0; j < TPT; ++j) {
-            float2 a;
-            sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
-            decays<EXACT>(mul2(k, r[j]), slow, em1[j], a);
             float2 n = input_weight(em1[j]);
             const bool rs = RESET && ((rst >> j) & 1);
             if (rs) n = dup(1.0f);
@@ -635,34 +648,37 @@ __global__ void __launch_bounds__(TPB, 2)
             const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
             h = rs ? u : add2(h, fma2(em1[j], h, u));
         }
+        auto back = [&](auto is_slow) {
 #pragma unroll
-        for (int j = TPT - 1; j >= 0; --j) {
-            const bool rs = RESET && ((rst >> j) & 1);
-            const float2 x = Pair<T>::widen(*at(0, j));
-            g = add2(g, Pair<T>::widen(*at(3, j)));
-            const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
-            float2 a = add2(em1[j], dup(1.0f));
-            if (!slow) {  // a small decay as it is, not as 1 + em1
-                const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-                if (!(la.x >= -0.25f)) a.x = e.x;
-                if (!(la.y >= -0.25f)) a.y = e.y;
+            for (int j = TPT - 1; j >= 0; --j) {
+                const bool rs = RESET && ((rst >> j) & 1);
+                const float2 x = Pair<T>::widen(*at(0, j));
+                g = add2(g, Pair<T>::widen(*at(3, j)));
+                const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
+                float2 a = add2(em1[j], dup(1.0f));
+                if constexpr (!decltype(is_slow)::value) {  // a small decay as it is, not as 1 + em1
+                    const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
+                    a = make_float2(la.x >= -0.25f ? a.x : e.x, la.y >= -0.25f ? a.y : e.y);
+                }
+                // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
+                // gives a finite dla, times la = 0
+                const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
+                const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
+                const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
+                const float2 dx = mul2(mul2(g, n), i[j]);
+                const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
+                float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
+                if (rs) dla = dup(0.0f);
+                const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
+                if (j < left) sum = fma2(dla, r[j], sum);
+                g = rs ? dup(0.0f) : fma2(em1[j], g, g);
+                *at(0, j) = Pair<T>::narrow(dx);
+                *at(1, j) = Pair<T>::narrow(dgx);
+                *at(2, j) = Pair<T>::narrow(dga);
             }
-            // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
-            // gives a finite dla, times la = 0
-            const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
-            const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
-            const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
-            const float2 dx = mul2(mul2(g, n), i[j]);
-            const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
-            float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
-            if (rs) dla = dup(0.0f);
-            const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
-            if (j < left) sum = fma2(dla, r[j], sum);
-            g = rs ? dup(0.0f) : fma2(em1[j], g, g);
-            *at(0, j) = Pair<T>::narrow(dx);
-            *at(1, j) = Pair<T>::narrow(dgx);
-            *at(2, j) = Pair<T>::narrow(dga);
-        }
+        };
+        if (slow) back(std::true_type());
+        else back(std::false_type());
         tc::fence_smem_async();
         __syncwarp();
         if (lane == 0) {
@@ -715,7 +731,7 @@ __global__ void __launch_bounds__(256) gated_update_kernel(GatedUpdateParams p) 
     float2 r, ii, em1, a;
     sigmas<EXACT>(one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_a)[i]), -87.0f),
                   one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_x)[i]), -41.5f), r, ii);
-    decays<EXACT>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), false, em1, a);
+    decays<EXACT, false>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), em1, a);
     if (rs) em1 = dup(-1.0f);
     const float h = p.state[i];
     const float hn = (rs ? 0.0f : fmaf(em1.x, h, h)) +
@@ -734,34 +750,80 @@ int device_sms() {
     return n;
 }
 
-// CTAs per cluster: the smallest power of two that gives every SM two CTAs, as
-// long as the sequence has tiles for them.
-int cluster_size(int64_t blocks, int64_t seqlen, int tile) {
-    if (const char* e = getenv("DEV_CL")) return atoi(e);
-    int cl = 1;
-    const int64_t want = 2 * static_cast<int64_t>(device_sms());
-    while (cl < kMaxCluster && blocks * cl < want && static_cast<int64_t>(cl) * tile < seqlen) cl *= 2;
-    return cl;
-}
-
-template <typename Kern, typename... Args>
-cudaError_t launch_clusters(Kern kern, int64_t blocks, int64_t batch, int cl, size_t smem, cudaStream_t s,
-                            const Args&... args) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess && cl > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int threads, int64_t blocks, int64_t batch, int cl,
+                                  size_t smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * cl), static_cast<unsigned>(batch));
-    cfg.blockDim = dim3(TPB);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr->id = cudaLaunchAttributeClusterDimension;
+    attr->val.clusterDim.x = static_cast<unsigned>(cl);
+    attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cl > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
+    return cfg;
+}
+
+// CTAs per cluster.  More of them cut the rounds a sequence takes, but share the
+// SMs, add an exchange per round and, beyond what the device holds at once
+// (asked of the runtime, once per device), run in waves.  A round measured
+// about 1.3 + 0.5 k us with k CTAs on an SM, and 0.7 us more in a cluster; the
+// size with the least waves x rounds x that is taken.  (b1 L65536 C1536: 15,
+// 256 us; 10, 281 us; 8, 345 us.  b8 L4096 C2048: 1, 145 us; 2, 158 us.)
+constexpr int kMaxDevices = 64;
+template <typename Kern>
+int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern kern, int threads, size_t smem,
+                 int64_t blocks, int64_t batch, int64_t seqlen) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return 1;
+    }
+    const double sms = device_sms();
+    const int64_t clusters = blocks * batch, tiles = (seqlen + TILE - 1) / TILE;
+    int best = 1;
+    double least = 0.0;
+    for (int cl = 1; cl <= kMaxCluster && cl <= tiles; ++cl) {
+        int n = held[dev][cl].load(std::memory_order_relaxed);  // clusters at once; 0 = not asked, -1 = none
+        if (n == 0) {
+            cudaLaunchAttribute attr;
+            cudaLaunchConfig_t cfg = cluster_config(&attr, threads, 1, 1, cl, smem, nullptr);
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+                cudaGetLastError();
+                n = -1;
+            }
+            held[dev][cl].store(n, std::memory_order_relaxed);
+        }
+        if (n < 1) continue;
+        const int64_t waves = (clusters + n - 1) / n, rounds = (tiles + cl - 1) / cl;
+        const double share = static_cast<double>(clusters < n ? clusters : n) * cl / sms;
+        const double cost = static_cast<double>(waves * rounds) *
+                            (1.3 + 0.5 * (share < 1.0 ? 1.0 : share) + (cl > 1 ? 0.7 : 0.0));
+        if (least == 0.0 || cost < least) {
+            least = cost;
+            best = cl;
+        }
+    }
+    return best;
+}
+
+// T, BWD: one table of held clusters per kernel family.
+template <typename T, bool BWD, typename Kern, typename... Args>
+cudaError_t launch_clusters(Kern kern, int threads, const GatedScanParams& p, size_t smem, cudaStream_t s,
+                            int* cluster, const Args&... args) {
+    static std::atomic<int> held[kMaxDevices][kMaxCluster + 1];
+    // (attributes are the device's own: set on every call)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (p.channels + CPB - 1) / CPB;
+    const int cl = cluster_size(held, kern, threads, smem, blocks, p.batch, p.seqlen);
+    *cluster = cl;
+    cudaLaunchAttribute attr;
+    const cudaLaunchConfig_t cfg = cluster_config(&attr, threads, blocks, p.batch, cl, smem, s);
+    return cudaLaunchKernelEx(&cfg, kern, p, args..., cl, static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP)));
 }
 
 }  // namespace
@@ -771,26 +833,20 @@ size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
 }
 
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
-    const int64_t blocks = (p.channels + CPB - 1) / CPB;
-    const int cl = cluster_size(blocks * p.batch, p.seqlen, TILE);
     const size_t smem = NW * kStages<T> * 3 * kTileBytes<T>;
-    const int wh = static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP));
     ScanMaps m;
-    const bool bf16 = sizeof(T) == 2;
-    if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, TPT) ||
-        !make_tmap_rows(&m.gate_a, p.gate_a, bf16, p.channels, p.seqlen, p.batch, TPT) ||
-        !make_tmap_rows(&m.gate_x, p.gate_x, bf16, p.channels, p.seqlen, p.batch, TPT) ||
-        !make_tmap_rows(&m.y, p.y, bf16, p.channels, p.seqlen, p.batch, TPT))
-        return cudaErrorInvalidValue;
-    return p.reset ? launch_clusters(gated_scan_kernel<T, true>, blocks, p.batch, cl, smem, s, p, m, cl, wh)
-                   : launch_clusters(gated_scan_kernel<T, false>, blocks, p.batch, cl, smem, s, p, m, cl, wh);
+    const std::pair<CUtensorMap*, const void*> arrays[] = {
+        {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.y, p.y}};
+    for (const auto& a : arrays)
+        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TPT))
+            return cudaErrorInvalidValue;
+    int cl = 1;
+    return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, kFwdThreads, p, smem, s, &cl, m)
+                   : launch_clusters<T, false>(gated_scan_kernel<T, false>, kFwdThreads, p, smem, s, &cl, m);
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {
-    const int64_t blocks = (p.channels + CPB - 1) / CPB;
-    const int cl = cluster_size(blocks * p.batch, p.seqlen, TILE);
     const size_t smem = NW * kStagesBwd<T> * 4 * kTileBytes<T>;
-    const int wh = static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP));
     ScanBwdMaps m;
     const std::pair<CUtensorMap*, const void*> arrays[] = {
         {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.dy, p.dy},
@@ -798,9 +854,10 @@ template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p
     for (const auto& a : arrays)
         if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TPT))
             return cudaErrorInvalidValue;
+    int cl = 1;
     const cudaError_t e =
-        p.reset ? launch_clusters(gated_scan_bwd_kernel<T, true>, blocks, p.batch, cl, smem, s, p, m, cl, wh)
-                : launch_clusters(gated_scan_bwd_kernel<T, false>, blocks, p.batch, cl, smem, s, p, m, cl, wh);
+        p.reset ? launch_clusters<T, true>(gated_scan_bwd_kernel<T, true>, kBwdThreads, p, smem, s, &cl, m)
+                : launch_clusters<T, true>(gated_scan_bwd_kernel<T, false>, kBwdThreads, p, smem, s, &cl, m);
     if (e != cudaSuccess) return e;
     return launch_kernel(gated_scan_finish_kernel, dim3(static_cast<unsigned>((p.channels + 31) / 32)),
                          dim3(kColSumThreads), 0, s, true, p, p.batch * cl);
