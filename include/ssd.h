@@ -435,9 +435,9 @@ typedef struct {
 
 ssd_status ssd_causal_conv1d(const ssd_conv1d_args* args, void* stream);
 
-/* Synchronises `stream` and returns SSD_ERR_TIMEOUT if a ssd_causal_conv1d
- * launch on this device timed out on an internal wait since the last check
- * (the flag is cleared), else SSD_OK. */
+/* Synchronises `stream` and returns SSD_ERR_TIMEOUT if a ssd_causal_conv1d or
+ * ssd_causal_conv1d_bwd launch on this device timed out on an internal wait
+ * since the last check (the flag is cleared), else SSD_OK. */
 ssd_status ssd_conv1d_check_status(void* stream);
 
 /* Gradients of ssd_causal_conv1d: of J = sum dy . y + d_final : final_state

@@ -738,9 +738,11 @@ ssd_status ssd_causal_conv1d(const ssd_conv1d_args* a, void* stream) {
 }
 
 ssd_status ssd_conv1d_check_status(void* stream) {
-    int v = 0;
-    if (ssd::conv1d_take_status(&v, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    int v = 0, w = 0;
+    if (ssd::conv1d_take_status(&v, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+        ssd::conv1d_bwd_take_status(&w, static_cast<cudaStream_t>(stream)) != cudaSuccess)
         return SSD_ERR_CUDA;
+    if (v == 0) v = w;
     return v == 0 ? SSD_OK : static_cast<ssd_status>(v);
 }
 
@@ -774,7 +776,8 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* a, void* stream) {
 
 size_t ssd_causal_conv1d_bwd_workspace_size(const ssd_conv1d_bwd_args* a) {
     if (check_conv_bwd_sizes(a) != SSD_OK) return 0;
-    return round_up(ssd::conv1d_bwd_partial_bytes(a->batch, a->seqlen, a->channels, a->width));
+    return round_up(ssd::conv1d_bwd_partial_bytes(a->batch, a->seqlen, a->channels, a->width,
+                                                  a->dtype == SSD_BF16));
 }
 
 ssd_status ssd_causal_conv1d_bwd(const ssd_conv1d_bwd_args* a, void* stream) {

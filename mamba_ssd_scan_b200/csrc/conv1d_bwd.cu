@@ -1,16 +1,21 @@
 // conv1d_bwd.cu -- the gradients of the causal depthwise convolution (the
 // formulas stand in include/ssd.h).
 //
-// A warp takes 64 channels (a pair per lane) over a segment of the sequence
-// and walks its tokens with two sliding windows in registers: the K inputs
-// that feed the token's output, and the last K gradients before the
-// activation, whose weighted sum is the gradient of the input K - 1 tokens
-// back.  A segment runs K - 1 tokens past its end to finish its inputs'
-// gradients (it recomputes those tokens' gradients; their share of dweight
-// belongs to the next segment).  The warps of a CTA take consecutive segments
-// and add their dweight and dbias in shared memory; one row per CTA goes to
-// the workspace, and a second kernel adds the rows in order.
+// Bandwidth-bound: x and dy are read once and dx written once.  A warp takes 64
+// channels (a pair per lane) over a segment of the sequence, in batches of 8
+// tokens that TMA brings into its own ring of shared-memory tiles.  It keeps
+// two windows in registers: the K inputs that feed a token's output, and the
+// last K gradients before the activation, whose weighted sum is the gradient
+// of the input K - 1 tokens back.  dx takes the place of x in the tile and
+// leaves by a TMA store; a segment's first and last K - 1 rows, which its
+// neighbours' tiles overlap, go out directly.  A segment runs K - 1 tokens past
+// its end to finish its inputs' gradients (it forms those tokens' gradients
+// again; their share of dweight belongs to the next segment).  Each warp
+// leaves its sums of dweight and dbias in a row of the workspace, and a second
+// kernel adds the rows in order.
 #include "mixers.h"
+#include "rows_tma.cuh"
+#include "tcgen05.cuh"
 #include "vec16.cuh"
 
 namespace ssd {
@@ -18,26 +23,81 @@ namespace {
 
 constexpr int NW = 8;     // warps (segments) per CTA
 constexpr int CPW = 64;   // channels per warp
+constexpr int TB = 8;     // tokens per batch (at least K - 1)
+template <typename T> constexpr int kRing = sizeof(T) == 2 ? 4 : 3;          // batches in shared memory
+template <typename T> constexpr int kRowBytes = CPW * sizeof(T);
+template <typename T> constexpr int kWarpBytes = kRing<T> * 2 * TB * kRowBytes<T>;  // x and dy tiles
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+// SSD_ERR_TIMEOUT once a launch gave up on a wait; read and cleared by
+// ssd_conv1d_check_status.
+__device__ int g_conv_bwd_status;
+
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-
-// silu'(o) = sg (1 + o (1 - sg)), sg = sigma(o)
-__device__ __forceinline__ float dsilu(float o) {
-    const float sg = 1.0f / (1.0f + __expf(-o));
-    return sg * fmaf(o, 1.0f - sg, 1.0f);
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float ex2_approx(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float rcp_approx(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+// silu'(o) = sg (1 + o (1 - sg)), sg = 1 / (1 + 2^(-o log2 e)); where the power
+// overflows, sg = 0
+__device__ __forceinline__ float2 dsilu2(float2 o) {
+    const float2 t = mul2(o, dup(-1.4426950408889634f));
+    const float2 d = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), dup(1.0f));
+    const float2 sg = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    return mul2(sg, fma2(o, fma2(sg, dup(-1.0f), dup(1.0f)), dup(1.0f)));
 }
 
+struct ConvBwdMaps {
+    CUtensorMap x, dy, dx;
+};
+
+// segments of seg tokens (a multiple of TB), nseg per (batch, channel block)
 template <typename T, int K, bool ACT>
-__global__ void __launch_bounds__(NW * 32) conv1d_bwd_kernel(ConvBwdParams p, int64_t seg) {
+__global__ void __launch_bounds__(NW * 32, K <= 4 && sizeof(T) == 2 ? 3 : 2)
+    conv1d_bwd_kernel(ConvBwdParams p, const __grid_constant__ ConvBwdMaps maps, int64_t seg, int nseg, int64_t warps) {
     using P = Pair<T>;
-    __shared__ float2 red[NW][32];
+    using Raw = typename P::Raw;
+    constexpr int R = kRing<T>, KM = K - 1;
+    constexpr uint32_t kTile = TB * kRowBytes<T>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) uint64_t loaded[NW][R];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t L = p.seqlen, Cn = p.channels, b = blockIdx.z;
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * CPW + 2 * lane;
+    const int64_t wi = static_cast<int64_t>(blockIdx.x) * NW + warp;
+    if (lane == 0) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) tc::mbar_init(tc::smem_u32(&loaded[warp][r]), 1);
+        tc::fence_mbar_init();
+    }
+    __syncwarp();
+    if (wi >= warps) return;  // (warps are independent: no barrier follows)
+    const int64_t L = p.seqlen, Cn = p.channels;
+    const int64_t nblk = (Cn + CPW - 1) / CPW;
+    const int64_t s = wi / (nblk * p.batch), col = wi - s * (nblk * p.batch);  // neighbours: one row of blocks
+    const int64_t b = col / nblk, c0 = (col - b * nblk) * CPW, c = c0 + 2 * lane;
     const bool active = c < Cn;
-    const int64_t ta = (static_cast<int64_t>(blockIdx.y) * NW + warp) * seg;
-    const int64_t te = ta + seg < L ? ta + seg : L;
+    const int64_t ta = s * seg, te = ta + seg < L ? ta + seg : L;
+    const int nb = static_cast<int>((te - ta + TB - 1) / TB);  // whole batches, then one for the K - 1 tokens after
+    const int total = nb + (K > 1 ? 1 : 0);
+
+    uint8_t* ring = smem + warp * kWarpBytes<T>;
+    auto load = [&](int n) {
+        const uint32_t dst = tc::smem_u32(ring) + (n % R) * 2 * kTile, bar = tc::smem_u32(&loaded[warp][n % R]);
+        const int t = static_cast<int>(ta + static_cast<int64_t>(n) * TB);
+        tc::mbar_expect_tx(bar, 2 * kTile);
+        tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
+        tc::tma_load_rows(dst + kTile, &maps.dy, bar, static_cast<int>(c0), t, static_cast<int>(b));
+    };
+    if (lane == 0)
+        for (int n = 0; n < R && n < total; ++n) load(n);
+
     float2 w[K], dw[K], bias = dup(0.0f), db = dup(0.0f);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -46,81 +106,109 @@ __global__ void __launch_bounds__(NW * 32) conv1d_bwd_kernel(ConvBwdParams p, in
     }
     if (active && p.bias) bias = make_float2(p.bias[c], p.bias[c + 1]);
     const T* xb = static_cast<const T*>(p.x) + b * L * Cn + c;
-    const T* yb = static_cast<const T*>(p.dy) + b * L * Cn + c;
-    T* db_x = static_cast<T*>(p.dx) + b * L * Cn + c;
-    if (active && ta < L) {
-        float2 xw[K], dw_[K];  // xin[t-(K-1) .. t], do[t .. t-(K-1)]
+    T* dxb = static_cast<T*>(p.dx) + b * L * Cn + c;
+    // xw[KM + j]: the input of batch token j; xw[0 .. KM - 1] the K - 1 before.
+    // dv alike: the gradients before the activation.
+    float2 xw[KM + TB], dv[KM + TB];
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            dw_[k] = dup(0.0f);
-            const int64_t i = ta - K + k;  // shifted by one when token ta enters
-            if (k == 0) xw[k] = dup(0.0f);
-            else if (i >= 0) xw[k] = P::widen(*reinterpret_cast<const typename P::Raw*>(xb + i * Cn));
-            else if (p.init_state)
-                xw[k] = make_float2(p.init_state[(b * Cn + c) * (K - 1) + (K - 1 + i)],
-                                    p.init_state[(b * Cn + c + 1) * (K - 1) + (K - 1 + i)]);
-            else xw[k] = dup(0.0f);
-        }
-        const int64_t tend = te + K - 1;
-        for (int64_t t = ta; t < tend; ++t) {
-            float2 x = dup(0.0f), d = dup(0.0f);
-            if (t < L) {
-                x = P::widen(*reinterpret_cast<const typename P::Raw*>(xb + t * Cn));
-                d = P::widen(*reinterpret_cast<const typename P::Raw*>(yb + t * Cn));
-            }
+    for (int k = 0; k < KM; ++k) {
+        dv[k] = dup(0.0f);
+        xw[k] = dup(0.0f);
+        const int64_t i = ta - KM + k;
+        if (active && i >= 0) xw[k] = P::widen(*reinterpret_cast<const Raw*>(xb + i * Cn));
+        else if (active && p.init_state)
+            xw[k] = make_float2(p.init_state[(b * Cn + c) * KM + (KM + i)],
+                                p.init_state[(b * Cn + c + 1) * KM + (KM + i)]);
+    }
+    bool ok = true;
+    for (int n = 0; n < total; ++n) {
+        uint8_t* tile = ring + (n % R) * 2 * kTile + lane * sizeof(Raw);
+        const int64_t t0 = ta + static_cast<int64_t>(n) * TB;
+        const bool halo = n == nb;
+        ok &= tc::mbar_wait(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
 #pragma unroll
-            for (int k = 0; k + 1 < K; ++k) xw[k] = xw[k + 1];
-            xw[K - 1] = x;
-            if (ACT && t < L) {
+        for (int j = 0; j < TB; ++j) {
+            xw[KM + j] = P::widen(*reinterpret_cast<const Raw*>(tile + j * kRowBytes<T>));
+            float2 d = P::widen(*reinterpret_cast<const Raw*>(tile + kTile + j * kRowBytes<T>));
+            if (ACT) {
                 float2 o = bias;
 #pragma unroll
-                for (int k = 0; k < K; ++k) o = fma2(w[k], xw[k], o);
-                d.x *= dsilu(o.x);
-                d.y *= dsilu(o.y);
+                for (int k = 0; k < K; ++k) o = fma2(w[k], xw[j + k], o);
+                d = mul2(d, dsilu2(o));
             }
-            if (t < te) {
+            dv[KM + j] = d;
+        }
+        if (t0 + TB > L) {  // no gradient past the sequence's end, whatever the inputs before it
 #pragma unroll
-                for (int k = 0; k < K; ++k) dw[k] = fma2(d, xw[k], dw[k]);
-                db.x += d.x;
-                db.y += d.y;
-            }
+            for (int j = 0; j < TB; ++j)
+                if (t0 + j >= L) dv[KM + j] = dup(0.0f);
+        }
+        if (!halo) {
 #pragma unroll
-            for (int k = K - 1; k > 0; --k) dw_[k] = dw_[k - 1];
-            dw_[0] = d;
-            const int64_t i = t - (K - 1);
-            if (i < ta && !(ta == 0 && i < 0)) continue;
-            float2 g = dup(0.0f);
+            for (int j = 0; j < TB; ++j) {
 #pragma unroll
-            for (int k = 0; k < K; ++k) g = fma2(w[k], dw_[k], g);
-            if (t >= L && p.d_final) {
-                g.x += p.d_final[(b * Cn + c) * (K - 1) + (t - L)];
-                g.y += p.d_final[(b * Cn + c + 1) * (K - 1) + (t - L)];
-            }
-            if (i >= 0) {
-                *reinterpret_cast<typename P::Raw*>(db_x + i * Cn) = P::narrow(g);
-            } else if (p.d_init) {
-                p.d_init[(b * Cn + c) * (K - 1) + t] = g.x;
-                p.d_init[(b * Cn + c + 1) * (K - 1) + t] = g.y;
+                for (int k = 0; k < K; ++k) dw[k] = fma2(dv[KM + j], xw[j + k], dw[k]);
+                db = add2(db, dv[KM + j]);
             }
         }
-    }
-    // the CTA's sums, segment after segment; row [K + 1][Cn], dbias last
-    float* row = p.partial + (b * gridDim.y + blockIdx.y) * (K + 1) * Cn;
+        // row j: the gradient of input t0 + j - (K - 1)
+        float2 g[TB];
 #pragma unroll
-    for (int k = 0; k <= K; ++k) {
-        __syncthreads();
-        red[warp][lane] = k < K ? dw[k < K ? k : 0] : db;
-        __syncthreads();
-        if (warp == 0 && active) {
-            float2 v = dup(0.0f);
+        for (int j = 0; j < TB; ++j) {
+            g[j] = mul2(w[0], dv[KM + j]);
 #pragma unroll
-            for (int j = 0; j < NW; ++j) {
-                v.x += red[j][lane].x;
-                v.y += red[j][lane].y;
+            for (int k = 1; k < K; ++k) g[j] = fma2(w[k], dv[KM + j - k], g[j]);
+        }
+        if (t0 + TB > L && p.d_final && active) {  // inputs the final state repeats
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                const int64_t f = t0 + j - L;
+                if (f >= 0 && f < KM) {
+                    g[j].x += p.d_final[(b * Cn + c) * KM + f];
+                    g[j].y += p.d_final[(b * Cn + c + 1) * KM + f];
+                }
             }
-            *reinterpret_cast<float2*>(row + k * Cn + c) = v;
+        }
+        if (n > 0 && !halo) {
+#pragma unroll
+            for (int j = 0; j < TB; ++j) *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g[j]);
+            tc::fence_smem_async();
+        } else if (active) {
+#pragma unroll
+            for (int j = 0; j < TB; ++j) {
+                const int64_t i = t0 + j - KM;
+                if (halo ? (j < KM && i < te) : i >= ta) {
+                    if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g[j]);
+                } else if (n == 0 && i < 0 && p.d_init) {
+                    p.d_init[(b * Cn + c) * KM + (KM + i)] = g[j].x;
+                    p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g[j].y;
+                }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KM; ++k) {
+            xw[k] = xw[TB + k];
+            dv[k] = dv[TB + k];
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (n > 0 && !halo) {
+                tc::tma_store_rows(&maps.dx, tc::smem_u32(ring) + (n % R) * 2 * kTile, static_cast<int>(c0),
+                                   static_cast<int>(t0 - KM), static_cast<int>(b));
+            }
+            tc::bulk_commit_group();
+            // the previous batch's store has read its tile: it takes the batch R - 1 ahead
+            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+            if (n > 0 && n - 1 + R < total) load(n - 1 + R);
         }
     }
+    if (lane == 0) tc::bulk_wait_all();
+    if (active) {  // row [K + 1][Cn], dbias last
+        float* row = p.partial + (b * nseg + s) * (K + 1) * Cn + c;
+#pragma unroll
+        for (int k = 0; k <= K; ++k) *reinterpret_cast<float2*>(row + k * Cn) = k < K ? dw[k < K ? k : 0] : db;
+    }
+    if (!ok) atomicExch(&g_conv_bwd_status, static_cast<int>(SSD_ERR_TIMEOUT));
 }
 
 __global__ void __launch_bounds__(kColSumThreads) conv1d_bwd_finish_kernel(ConvBwdParams p, int64_t rows) {
@@ -133,43 +221,61 @@ __global__ void __launch_bounds__(kColSumThreads) conv1d_bwd_finish_kernel(ConvB
     });
 }
 
-// Segments: enough warps for about eight per SM scheduler, at least 32 tokens
-// each (the K - 1 tokens past a segment's end are computed twice).
+// Segments: the number, up to one per 32 tokens, with the least waves x (tokens
+// of a segment + the tokens' worth of its start, end and sums, about 16), at
+// the 8 warps x 3 (bf16) or 2 CTAs an SM holds.
 struct ConvGrid {
-    int64_t seg, rows;
-    unsigned gx, gy;
+    int64_t seg, nseg, warps;
 };
-ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels) {
-    ConvGrid g;
-    const int64_t nblk = (channels + CPW - 1) / CPW;
-    const int64_t want = 148 * 32;  // warps
-    int64_t nseg = want / (nblk * batch);
-    if (nseg < 1) nseg = 1;
-    g.seg = (seqlen + nseg - 1) / nseg;
-    if (g.seg < 32) g.seg = 32;
-    nseg = (seqlen + g.seg - 1) / g.seg;
-    g.gx = static_cast<unsigned>(nblk);
-    g.gy = static_cast<unsigned>((nseg + NW - 1) / NW);
-    g.rows = batch * g.gy;
-    return g;
+ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels, int per_sm) {
+    const int64_t cols = (channels + CPW - 1) / CPW * batch, slots = int64_t{148} * per_sm * NW;
+    ConvGrid best{};
+    int64_t least = 0;
+    for (int64_t n = 1; n <= 1024 && (n == 1 || (seqlen + n - 1) / n >= 32); ++n) {
+        ConvGrid g;
+        g.seg = ((seqlen + n - 1) / n + TB - 1) / TB * TB;
+        g.nseg = (seqlen + g.seg - 1) / g.seg;
+        g.warps = cols * g.nseg;
+        const int64_t cost = (g.warps + slots - 1) / slots * (g.seg + 16);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = g;
+        }
+    }
+    return best;
+}
+
+template <typename T, int K, bool ACT>
+cudaError_t launch_act(const ConvBwdParams& p, const ConvBwdMaps& m, const ConvGrid& g, cudaStream_t s) {
+    const auto kern = conv1d_bwd_kernel<T, K, ACT>;
+    const int smem = NW * kWarpBytes<T>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>((g.warps + NW - 1) / NW), NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg),
+                                                                             g.warps);
+    return cudaGetLastError();
 }
 
 template <typename T, int K> cudaError_t launch_k(const ConvBwdParams& p, cudaStream_t s) {
-    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.channels);
-    const dim3 grid(g.gx, g.gy, static_cast<unsigned>(p.batch));
-    if (p.activation) conv1d_bwd_kernel<T, K, true><<<grid, NW * 32, 0, s>>>(p, g.seg);
-    else conv1d_bwd_kernel<T, K, false><<<grid, NW * 32, 0, s>>>(p, g.seg);
-    const cudaError_t e = cudaGetLastError();
+    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.channels, sizeof(T) == 2 ? 3 : 2);
+    ConvBwdMaps m;
+    const bool bf16 = sizeof(T) == 2;
+    if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, TB) ||
+        !make_tmap_rows(&m.dy, p.dy, bf16, p.channels, p.seqlen, p.batch, TB) ||
+        !make_tmap_rows(&m.dx, p.dx, bf16, p.channels, p.seqlen, p.batch, TB))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = p.activation ? launch_act<T, K, true>(p, m, g, s) : launch_act<T, K, false>(p, m, g, s);
     if (e != cudaSuccess) return e;
     const int64_t cols = (p.width + 1) * p.channels;
     return launch_kernel(conv1d_bwd_finish_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)),
-                         dim3(kColSumThreads), 0, s, true, p, g.rows);
+                         dim3(kColSumThreads), 0, s, true, p, p.batch * g.nseg);
 }
 
 }  // namespace
 
-size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width) {
-    return static_cast<size_t>(conv_grid(batch, seqlen, channels).rows) * (width + 1) * channels * sizeof(float);
+size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width, bool bf16) {
+    return static_cast<size_t>(batch * conv_grid(batch, seqlen, channels, bf16 ? 3 : 2).nseg) * (width + 1) *
+           channels * sizeof(float);
 }
 
 template <typename T> cudaError_t launch_conv1d_bwd(const ConvBwdParams& p, cudaStream_t s) {
@@ -188,5 +294,14 @@ template <typename T> cudaError_t launch_conv1d_bwd(const ConvBwdParams& p, cuda
 
 template cudaError_t launch_conv1d_bwd<float>(const ConvBwdParams&, cudaStream_t);
 template cudaError_t launch_conv1d_bwd<__nv_bfloat16>(const ConvBwdParams&, cudaStream_t);
+
+cudaError_t conv1d_bwd_take_status(int* v, cudaStream_t s) {
+    int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_conv_bwd_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess)
+        e = cudaMemcpyToSymbolAsync(g_conv_bwd_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    return e;
+}
 
 }  // namespace ssd
