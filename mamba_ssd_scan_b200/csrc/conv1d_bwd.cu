@@ -120,70 +120,70 @@ __global__ void __launch_bounds__(NW * 32, K <= 4 && sizeof(T) == 2 ? 3 : 2)
             xw[k] = make_float2(p.init_state[(b * Cn + c) * KM + (KM + i)],
                                 p.init_state[(b * Cn + c + 1) * KM + (KM + i)]);
     }
+    // token j of a batch: its input and its gradient before the activation
+    auto token = [&](const uint8_t* tile, int j) {
+        xw[KM + j] = P::widen(*reinterpret_cast<const Raw*>(tile + j * kRowBytes<T>));
+        float2 d = P::widen(*reinterpret_cast<const Raw*>(tile + kTile + j * kRowBytes<T>));
+        if (ACT) {
+            float2 o = bias;
+#pragma unroll
+            for (int k = 0; k < K; ++k) o = fma2(w[k], xw[j + k], o);
+            d = mul2(d, dsilu2(o));
+        }
+        dv[KM + j] = d;
+    };
+    auto sums = [&](int j) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) dw[k] = fma2(dv[KM + j], xw[j + k], dw[k]);
+        db = add2(db, dv[KM + j]);
+    };
+    // the gradient of the input K - 1 tokens before token j
+    auto input_gradient = [&](int j) {
+        float2 g = mul2(w[0], dv[KM + j]);
+#pragma unroll
+        for (int k = 1; k < K; ++k) g = fma2(w[k], dv[KM + j - k], g);
+        return g;
+    };
     bool ok = true;
     for (int n = 0; n < total; ++n) {
         uint8_t* tile = ring + (n % R) * 2 * kTile + lane * sizeof(Raw);
         const int64_t t0 = ta + static_cast<int64_t>(n) * TB;
         const bool halo = n == nb;
         ok &= tc::mbar_wait(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-            xw[KM + j] = P::widen(*reinterpret_cast<const Raw*>(tile + j * kRowBytes<T>));
-            float2 d = P::widen(*reinterpret_cast<const Raw*>(tile + kTile + j * kRowBytes<T>));
-            if (ACT) {
-                float2 o = bias;
-#pragma unroll
-                for (int k = 0; k < K; ++k) o = fma2(w[k], xw[j + k], o);
-                d = mul2(d, dsilu2(o));
-            }
-            dv[KM + j] = d;
-        }
-        if (t0 + TB > L) {  // no gradient past the sequence's end, whatever the inputs before it
-#pragma unroll
-            for (int j = 0; j < TB; ++j)
-                if (t0 + j >= L) dv[KM + j] = dup(0.0f);
-        }
-        if (!halo) {
+        if (n > 0 && !halo && t0 + TB <= L) {  // whole batches inside the segment, without a condition
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
-#pragma unroll
-                for (int k = 0; k < K; ++k) dw[k] = fma2(dv[KM + j], xw[j + k], dw[k]);
-                db = add2(db, dv[KM + j]);
+                token(tile, j);
+                sums(j);
+                *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(input_gradient(j));
             }
-        }
-        // row j: the gradient of input t0 + j - (K - 1)
-        float2 g[TB];
-#pragma unroll
-        for (int j = 0; j < TB; ++j) {
-            g[j] = mul2(w[0], dv[KM + j]);
-#pragma unroll
-            for (int k = 1; k < K; ++k) g[j] = fma2(w[k], dv[KM + j - k], g[j]);
-        }
-        if (t0 + TB > L && p.d_final && active) {  // inputs the final state repeats
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                const int64_t f = t0 + j - L;
-                if (f >= 0 && f < KM) {
-                    g[j].x += p.d_final[(b * Cn + c) * KM + f];
-                    g[j].y += p.d_final[(b * Cn + c + 1) * KM + f];
-                }
-            }
-        }
-        if (n > 0 && !halo) {
-#pragma unroll
-            for (int j = 0; j < TB; ++j) *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g[j]);
             tc::fence_smem_async();
-        } else if (active) {
+        } else {
 #pragma unroll
             for (int j = 0; j < TB; ++j) {
+                token(tile, j);
+                // no gradient past the sequence's end, whatever the inputs before it
+                if (t0 + j >= L) dv[KM + j] = dup(0.0f);
+                if (!halo) sums(j);
+                float2 g = input_gradient(j);
+                const int64_t f = t0 + j - L;
+                if (f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
+                    g.x += p.d_final[(b * Cn + c) * KM + f];
+                    g.y += p.d_final[(b * Cn + c + 1) * KM + f];
+                }
                 const int64_t i = t0 + j - KM;
-                if (halo ? (j < KM && i < te) : i >= ta) {
-                    if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g[j]);
-                } else if (n == 0 && i < 0 && p.d_init) {
-                    p.d_init[(b * Cn + c) * KM + (KM + i)] = g[j].x;
-                    p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g[j].y;
+                if (n > 0 && !halo) {
+                    *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g);
+                } else if (active) {
+                    if (halo ? (j < KM && i < te) : i >= ta) {
+                        if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g);
+                    } else if (n == 0 && i < 0 && p.d_init) {
+                        p.d_init[(b * Cn + c) * KM + (KM + i)] = g.x;
+                        p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g.y;
+                    }
                 }
             }
+            if (n > 0 && !halo) tc::fence_smem_async();
         }
 #pragma unroll
         for (int k = 0; k < KM; ++k) {
