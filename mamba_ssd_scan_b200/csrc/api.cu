@@ -776,8 +776,7 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* a, void* stream) {
 
 size_t ssd_causal_conv1d_bwd_workspace_size(const ssd_conv1d_bwd_args* a) {
     if (check_conv_bwd_sizes(a) != SSD_OK) return 0;
-    return round_up(ssd::conv1d_bwd_partial_bytes(a->batch, a->seqlen, a->channels, a->width,
-                                                  a->dtype == SSD_BF16));
+    return round_up(ssd::conv1d_bwd_partial_bytes(a->batch, a->seqlen, a->channels, a->width));
 }
 
 ssd_status ssd_causal_conv1d_bwd(const ssd_conv1d_bwd_args* a, void* stream) {

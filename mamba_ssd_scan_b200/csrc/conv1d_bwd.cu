@@ -24,6 +24,9 @@ namespace {
 constexpr int NW = 8;     // warps (segments) per CTA
 constexpr int CPW = 64;   // channels per warp
 constexpr int TB = 8;     // tokens per batch (at least K - 1)
+// CTAs per SM: two, whose 128 registers a thread let the tokens of a batch overlap
+// (b8 L4096 C2304 K4: 101 us; three at 80 registers 109, four at 64 130)
+constexpr int kPerSm = 2;
 template <typename T> constexpr int kRing = sizeof(T) == 2 ? 4 : 3;          // batches in shared memory
 template <typename T> constexpr int kRowBytes = CPW * sizeof(T);
 template <typename T> constexpr int kWarpBytes = kRing<T> * 2 * TB * kRowBytes<T>;  // x and dy tiles
@@ -61,7 +64,7 @@ struct ConvBwdMaps {
 
 // segments of seg tokens (a multiple of TB), nseg per (batch, channel block)
 template <typename T, int K, bool ACT>
-__global__ void __launch_bounds__(NW * 32, K <= 4 && sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(NW * 32, kPerSm)
     conv1d_bwd_kernel(ConvBwdParams p, const __grid_constant__ ConvBwdMaps maps, int64_t seg, int nseg, int64_t warps) {
     using P = Pair<T>;
     using Raw = typename P::Raw;
@@ -223,12 +226,12 @@ __global__ void __launch_bounds__(kColSumThreads) conv1d_bwd_finish_kernel(ConvB
 
 // Segments: the number, up to one per 32 tokens, with the least waves x (tokens
 // of a segment + the tokens' worth of its start, end and sums, about 16), at
-// the 8 warps x 3 (bf16) or 2 CTAs an SM holds.
+// the warps the device holds at once.
 struct ConvGrid {
     int64_t seg, nseg, warps;
 };
-ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels, int per_sm) {
-    const int64_t cols = (channels + CPW - 1) / CPW * batch, slots = int64_t{148} * per_sm * NW;
+ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels) {
+    const int64_t cols = (channels + CPW - 1) / CPW * batch, slots = int64_t{148} * kPerSm * NW;
     ConvGrid best{};
     int64_t least = 0;
     for (int64_t n = 1; n <= 1024 && (n == 1 || (seqlen + n - 1) / n >= 32); ++n) {
@@ -257,7 +260,7 @@ cudaError_t launch_act(const ConvBwdParams& p, const ConvBwdMaps& m, const ConvG
 }
 
 template <typename T, int K> cudaError_t launch_k(const ConvBwdParams& p, cudaStream_t s) {
-    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.channels, sizeof(T) == 2 ? 3 : 2);
+    const ConvGrid g = conv_grid(p.batch, p.seqlen, p.channels);
     ConvBwdMaps m;
     const bool bf16 = sizeof(T) == 2;
     if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, TB) ||
@@ -273,8 +276,8 @@ template <typename T, int K> cudaError_t launch_k(const ConvBwdParams& p, cudaSt
 
 }  // namespace
 
-size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width, bool bf16) {
-    return static_cast<size_t>(batch * conv_grid(batch, seqlen, channels, bf16 ? 3 : 2).nseg) * (width + 1) *
+size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width) {
+    return static_cast<size_t>(batch * conv_grid(batch, seqlen, channels).nseg) * (width + 1) *
            channels * sizeof(float);
 }
 

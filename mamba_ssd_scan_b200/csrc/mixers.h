@@ -91,7 +91,7 @@ struct ConvBwdParams {
     float* partial;            // workspace: rows of [width + 1][channels]
 };
 template <typename T> cudaError_t launch_conv1d_bwd(const ConvBwdParams& p, cudaStream_t s);
-size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width, bool bf16);
+size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width);
 // Copies the gradient's device status word to *v and clears it (synchronises s).
 cudaError_t conv1d_bwd_take_status(int* v, cudaStream_t s);
 
