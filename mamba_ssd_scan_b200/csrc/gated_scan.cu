@@ -186,19 +186,23 @@ __device__ __forceinline__ void store_async(uint32_t dst, int v, uint32_t mbar) 
                  : "r"(dst), "r"(v), "r"(mbar)
                  : "memory");
 }
-// bounded wait on a local mbarrier that peers complete; false once aborted
-__device__ __forceinline__ bool wait_cluster(uint32_t mbar, uint32_t parity, volatile int* abort) {
-    for (uint32_t i = 0; i < tc::kSpinLimit; ++i) {
+// Bounded wait on an mbarrier of this CTA (that peers of the cluster may
+// complete); false once aborted.  A probe suspends the warp until the phase
+// completes or 2 us have passed: short ones would take issue slots from the
+// warps that form gates.
+constexpr uint32_t kProbes = 1u << 19, kProbeNs = 2000;
+__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, volatile int* abort) {
+    for (uint32_t i = 0; i < kProbes; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
             "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}\n"
             : "=r"(ok)
-            : "r"(mbar), "r"(parity), "r"(200)
+            : "r"(mbar), "r"(parity), "r"(kProbeNs)
             : "memory");
         if (ok) return true;
-        if ((i & 63) == 63 && *abort) return false;
+        if ((i & 15) == 15 && *abort) return false;
     }
     *abort = 1;
     return false;
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
         bool ok = true;  // (whole-warp: no map is sent, received or waited for after a timeout)
         for (int it = 0; it < rounds; ++it) {
             const int buf = it & 1;
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+            if (ok) ok = wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
             ok = __all_sync(0xffffffffu, ok);
             float4 g[NW];
             uint32_t rst = 0;
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
                     if (RESET && lane < cl)
                         store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
                 }
-                ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+                ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, &ex.abort));
                 for (int q = 0; q < cl; ++q) {
                     if (q == rank) h = carry;
                     carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
             // the outputs, over gate_a's tile, and out
-            if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+            if (ok) ok = wait_phase(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
             float2 h = ex.entering[warp][lane];
             // a tile starts at a multiple of the interval: group 0 keeps its state
             if (warp == 0 && p.states && active && left > 0)
@@ -513,7 +517,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         const int buf = it & 1;
         float2 h = next;
         next = kept(it + 1);
-        if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
+        if (ok) ok = wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
         ok = __all_sync(0xffffffffu, ok);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
@@ -545,7 +549,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
                 if (RESET && lane < cl)
                     store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
             }
-            ok = __all_sync(0xffffffffu, wait_cluster(bar, (it >> 1) & 1, &ex.abort));
+            ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, &ex.abort));
             for (int q = cl - 1; q >= 0; --q) {
                 if (q == rank) cin = carry;
                 carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
             }
         }
         if (warp == 0) ok = hand_out(it, ok);
-        else if (ok) ok = tc::wait_or_abort(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+        else if (ok) ok = wait_phase(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
         const float4 in = ex.entering[warp][lane];
         float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
         float2 hp[TPT];
