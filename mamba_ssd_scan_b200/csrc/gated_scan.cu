@@ -187,12 +187,13 @@ __device__ __forceinline__ void store_async(uint32_t dst, int v, uint32_t mbar) 
                  : "memory");
 }
 // Bounded wait on an mbarrier of this CTA (that peers of the cluster may
-// complete); false once aborted.  A probe suspends the warp until the phase
-// completes or 2 us have passed: short ones would take issue slots from the
-// warps that form gates.
-constexpr uint32_t kProbes = 1u << 19, kProbeNs = 2000;
-__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, volatile int* abort) {
-    for (uint32_t i = 0; i < kProbes; ++i) {
+// complete).  A probe suspends the warp until the phase completes or 2 us have
+// passed.  On expiry the CTA's abort flag is raised.  Waits on a peer give up
+// after about a second, those on the CTA's own warps and loads after four, so
+// that they outlast it.
+constexpr uint32_t kPeerProbes = 1u << 19, kOwnProbes = 1u << 21, kProbeNs = 2000;
+__device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, uint32_t probes, volatile int* abort) {
+    for (uint32_t i = 0; i < probes; ++i) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
@@ -202,7 +203,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, volat
             : "r"(mbar), "r"(parity), "r"(kProbeNs)
             : "memory");
         if (ok) return true;
-        if ((i & 15) == 15 && *abort) return false;
     }
     *abort = 1;
     return false;
@@ -229,13 +229,14 @@ struct Exchange {
     float4 tile_map[2][kMaxCluster][32];  // the cluster's tiles, two rounds
     float2 entering[NW][32];              // the state entering each group
     int group_rst[NW], tile_rst[2][kMaxCluster];
-    uint64_t maps_ready, states_ready, tiles_ready[2], loaded[NW][2];
+    // the input tiles of a slot have landed; the groups' maps are written (and x
+    // and gate_x read); their entering states are; their outputs are
+    uint64_t loaded[2], maps_ready, states_ready, outputs_ready, tiles_ready[2];
     int abort;
 };
 
-// A warp's ring of input tiles (TPT rows of 64 channels): two rounds ahead for
-// bf16; one for fp32, whose tiles are twice as large, so that three CTAs still
-// share an SM.
+// The ring of input tiles (64 rows of 64 channels): two rounds for bf16; one for
+// fp32, whose tiles are twice as large, so that three CTAs still share an SM.
 template <typename T> constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
 template <typename T> constexpr int kRowBytes = CPB * sizeof(T);
 template <typename T> constexpr int kTileBytes = TPT * kRowBytes<T>;
@@ -248,9 +249,9 @@ template <typename T, bool RESET>
 __global__ void __launch_bounds__(kFwdThreads, 3)
     gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
-    constexpr int ST = kStages<T>, TB = kTileBytes<T>;
+    constexpr int ST = kStages<T>, TB = kTileBytes<T>, CB = NW * TB;
     using Raw = typename Pair<T>::Raw;
-    extern __shared__ __align__(128) uint8_t ring[];    // [NW][ST][3] tiles: x, gate_x, gate_a (then y)
+    extern __shared__ __align__(128) uint8_t ring[];    // [ST][3] tiles: x, gate_x, gate_a (then y)
     __shared__ Exchange ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
@@ -261,29 +262,52 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
     const int rounds = static_cast<int>((L + round - 1) / round);
     if (threadIdx.x == 0) {
         tc::mbar_init(tc::smem_u32(&ex.maps_ready), NW);
+        tc::mbar_init(tc::smem_u32(&ex.outputs_ready), NW);
         tc::mbar_init(tc::smem_u32(&ex.states_ready), 1);
-        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[0]), 1);
-        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[1]), 1);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            tc::mbar_init(tc::smem_u32(&ex.loaded[w][0]), 1);
-            tc::mbar_init(tc::smem_u32(&ex.loaded[w][1]), 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(tc::smem_u32(&ex.tiles_ready[i]), 1);
+            tc::mbar_init(tc::smem_u32(&ex.loaded[i]), 1);
         }
         tc::fence_mbar_init();
         ex.abort = 0;
     }
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // every CTA's barriers exist before a peer completes on them
+    const int64_t first = static_cast<int64_t>(rank) * TILE;  // the tile's first token, round 0
 
     if (warp == NW) {
+        // The ninth warp: the tiles' loads and stores (lane 0), and the maps.
+        // x and gate_x of round n arm the slot's barrier for all three; gate_a's
+        // place holds y until its store has read it.
+        const uint32_t tiles = tc::smem_u32(ring);
+        const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
+        auto load_x = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 3 * CB, bar = tc::smem_u32(&ex.loaded[n % ST]);
+            const int t = static_cast<int>(first + n * round);
+            tc::mbar_expect_tx(bar, 3 * CB);
+            tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
+            tc::tma_load_rows(dst + CB, &maps.gate_x, bar, ci, t, bi);
+        };
+        auto load_a = [&](int n) {
+            tc::tma_load_rows(tiles + (n % ST) * 3 * CB + 2 * CB, &maps.gate_a, tc::smem_u32(&ex.loaded[n % ST]), ci,
+                              static_cast<int>(first + n * round), bi);
+        };
+        if (lane == 0) {
+            for (int n = 0; n < ST && n < rounds; ++n) {
+                load_x(n);
+                load_a(n);
+            }
+        }
         float2 carry = (active && p.init_state) ? *reinterpret_cast<const float2*>(p.init_state + b * C + c)
                                                 : dup(0.0f);
         const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
         bool ok = true;  // (whole-warp: no map is sent, received or waited for after a timeout)
         for (int it = 0; it < rounds; ++it) {
             const int buf = it & 1;
-            if (ok) ok = wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
-            ok = __all_sync(0xffffffffu, ok);
+            // the compute warps' arrivals depend on no other CTA: waited for in any case
+            wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, kOwnProbes, &ex.abort);
+            if (lane == 0 && it + ST < rounds) load_x(it + ST);
             float4 g[NW];
             uint32_t rst = 0;
 #pragma unroll
@@ -310,7 +334,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
                     if (RESET && lane < cl)
                         store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
                 }
-                ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, &ex.abort));
+                ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, kPeerProbes, &ex.abort));
                 for (int q = 0; q < cl; ++q) {
                     if (q == rank) h = carry;
                     carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -324,122 +348,86 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
             if (cl == 1) carry = h;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+            wait_phase(tc::smem_u32(&ex.outputs_ready), it & 1, kOwnProbes, &ex.abort);
+            if (lane == 0) {
+                const int64_t t = first + it * round;
+                if (t < L) {
+                    tc::tma_store_rows(&maps.y, tiles + (it % ST) * 3 * CB + 2 * CB, ci, static_cast<int>(t), bi);
+                    tc::bulk_commit_group();
+                }
+                if (it + ST < rounds) {
+                    tc::bulk_wait_read_all();  // y has left its place
+                    load_a(it + ST);
+                }
+            }
         }
         if (p.final_state && active && rank == 0)
             *reinterpret_cast<float2*>(p.final_state + b * C + c) = carry;
+        if (lane == 0) tc::bulk_wait_all();
     } else {
-        int64_t t0 = static_cast<int64_t>(rank) * TILE + warp * TPT;  // the group's first token
         const int64_t nst = (L + kInterval - 1) / kInterval;
-        const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 3 * TB;
-        // lane 0 loads round n's tiles into their slot: x and gate_x, which
-        // arms the slot's barrier for all three, and gate_a, whose place holds y
-        // until its store has read it
-        auto load_x = [&](int n) {
-            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-            const int t = static_cast<int>(t0 + n * round);
-            tc::mbar_expect_tx(bar, 3 * TB);
-            tc::tma_load_rows(dst, &maps.x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-            tc::tma_load_rows(dst + TB, &maps.gate_x, bar, static_cast<int>(c0), t, static_cast<int>(b));
-        };
-        auto load_a = [&](int n) {
-            const uint32_t dst = tiles + (n % ST) * 3 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-            tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, static_cast<int>(c0),
-                              static_cast<int>(t0 + n * round), static_cast<int>(b));
-        };
-        if (lane == 0) {
-            for (int n = 0; n < ST && n < rounds; ++n) {
-                load_x(n);
-                load_a(n);
-            }
-        }
         const float2 k = decay_rates(p, c, active);
         const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-        const int64_t first = t0;
-        bool ok = true;
-        bool flag = RESET && reset_flag(p.reset, b, t0, L, lane);
-        for (int it = 0; it < rounds; ++it) {
-            const int64_t t = first + it * round;
+        int64_t t = first + warp * TPT;  // the group's first token
+        bool flag = RESET && reset_flag(p.reset, b, t, L, lane);
+        uint8_t* const mine = ring + warp * TB + lane * sizeof(Raw);
+        for (int it = 0; it < rounds; ++it, t += round) {
             const int slot = it % ST;
-            const uint8_t* src = ring + (warp * ST + slot) * 3 * TB + lane * sizeof(Raw);
+            uint8_t* src = mine + slot * 3 * CB;
+            auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * CB + j * kRowBytes<T>); };
             uint32_t rst = 0;
             if constexpr (RESET) {
                 rst = __ballot_sync(0xffffffffu, flag);
                 flag = reset_flag(p.reset, b, t + round, L, lane);
             }
-            if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+            wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
             // the gates and the group's map
             float2 em1[TPT], u[TPT];
             auto form = [&](auto is_slow) {
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
-                    const uint8_t* row = src + j * kRowBytes<T>;
                     float2 r, i, a;
-                    sigmas<EXACT>(read_gates(*reinterpret_cast<const Raw*>(row + 2 * TB), kLeastA),
-                                  read_gates(*reinterpret_cast<const Raw*>(row + TB), kLeastX), r, i);
+                    sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r, i);
                     decays<EXACT, decltype(is_slow)::value>(mul2(k, r), em1[j], a);
                     float2 n = input_weight(em1[j]);
                     if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
-                    u[j] = mul2(mul2(n, i), Pair<T>::widen(*reinterpret_cast<const Raw*>(row)));
+                    u[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
                 }
             };
             if (slow) form(std::true_type());
             else form(std::false_type());
-            __syncwarp();
-            if (lane == 0) {
-                if (ST == 2 && it > 0 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();  // the previous round's y has left
-                    load_a(it + 1);
-                }
-                if (it + ST < rounds) load_x(it + ST);
-            }
-            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-            if (left < TPT) {  // tokens past the end change nothing
+            if (t + TPT > L) {  // tokens past the end change nothing
 #pragma unroll
                 for (int j = 0; j < TPT; ++j)
-                    if (j >= left) em1[j] = u[j] = dup(0.0f);
+                    if (t + j >= L) em1[j] = u[j] = dup(0.0f);
             }
             float2 A = dup(1.0f), H = dup(0.0f);
 #pragma unroll
             for (int j = 0; j < TPT; ++j) {
-                if (RESET && ((rst >> j) & 1)) {
-                    A = dup(0.0f);
-                    H = u[j];
-                } else {
-                    A = fma2(em1[j], A, A);
-                    H = add2(H, fma2(em1[j], H, u[j]));
-                }
+                const bool rs = RESET && ((rst >> j) & 1);
+                A = rs ? dup(0.0f) : fma2(em1[j], A, A);
+                H = rs ? u[j] : add2(H, fma2(em1[j], H, u[j]));
             }
             ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
             if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-            // the outputs, over gate_a's tile, and out
-            if (ok) ok = wait_phase(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+            // the outputs, over gate_a's tile; the ninth warp's wait on its cluster is
+            // bounded and it always arrives
+            wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
             float2 h = ex.entering[warp][lane];
             // a tile starts at a multiple of the interval: group 0 keeps its state
-            if (warp == 0 && p.states && active && left > 0)
+            if (warp == 0 && p.states && active && t < L)
                 *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
 #pragma unroll
             for (int j = 0; j < TPT; ++j) {
-                if (RESET && ((rst >> j) & 1)) h = u[j];
-                else h = add2(h, fma2(em1[j], h, u[j]));
-                *reinterpret_cast<Raw*>(const_cast<uint8_t*>(src) + 2 * TB + j * kRowBytes<T>) = Pair<T>::narrow(h);
+                h = RESET && ((rst >> j) & 1) ? u[j] : add2(h, fma2(em1[j], h, u[j]));
+                *at(2, j) = Pair<T>::narrow(h);
             }
             tc::fence_smem_async();
             __syncwarp();
-            if (lane == 0) {
-                if (left > 0) {
-                    tc::tma_store_rows(&maps.y, tiles + slot * 3 * TB + 2 * TB, static_cast<int>(c0),
-                                       static_cast<int>(t), static_cast<int>(b));
-                    tc::bulk_commit_group();
-                }
-                if (ST == 1 && it + 1 < rounds) {
-                    tc::bulk_wait_read_all();
-                    load_a(it + 1);
-                }
-            }
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
         }
-        if (lane == 0) tc::bulk_wait_all();
     }
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
@@ -517,8 +505,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         const int buf = it & 1;
         float2 h = next;
         next = kept(it + 1);
-        if (ok) ok = wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, &ex.abort);
-        ok = __all_sync(0xffffffffu, ok);
+        wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, kOwnProbes, &ex.abort);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
@@ -549,7 +536,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
                 if (RESET && lane < cl)
                     store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
             }
-            ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, &ex.abort));
+            ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, kPeerProbes, &ex.abort));
             for (int q = cl - 1; q >= 0; --q) {
                 if (q == rank) cin = carry;
                 carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -595,7 +582,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
             flag = it + 1 < rounds && reset_flag(p.reset, b, t - round, L, lane);
         }
         const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-        if (!tc::mbar_wait(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1)) ex.abort = 1;
+        wait_phase(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
         float2 r[TPT], i[TPT], em1[TPT];
         float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
         auto form = [&](auto is_slow) {
@@ -640,7 +627,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
             }
         }
         if (warp == 0) ok = hand_out(it, ok);
-        else if (ok) ok = wait_phase(tc::smem_u32(&ex.states_ready), it & 1, &ex.abort);
+        else wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
         const float4 in = ex.entering[warp][lane];
         float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
         float2 hp[TPT];
@@ -842,7 +829,7 @@ template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cu
     const std::pair<CUtensorMap*, const void*> arrays[] = {
         {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.y, p.y}};
     for (const auto& a : arrays)
-        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TPT))
+        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TILE))
             return cudaErrorInvalidValue;
     int cl = 1;
     return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, kFwdThreads, p, smem, s, &cl, m)
