@@ -33,8 +33,8 @@ constexpr int kInterval = SSD_GATED_SCAN_INTERVAL;
 constexpr int NW = 8;                   // groups per CTA, a warp each
 constexpr int kFwdThreads = (NW + 1) * 32;  // and the warp that composes their maps
 constexpr int kBwdThreads = NW * 32;
-constexpr int TPT = 8;           // tokens per group
-constexpr int TILE = NW * TPT;   // tokens per CTA and round
+constexpr int TPT = 8;           // the gradient's tokens per group
+constexpr int TILE = NW * TPT;   // and per CTA and round
 static_assert(TILE == kInterval, "a tile starts where a state is kept");
 constexpr int CPB = 64;          // channels per CTA
 constexpr int kMaxCluster = 16;
@@ -213,8 +213,9 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, uint3
 __device__ int g_gated_status;
 
 // restarts among the group's tokens: lane j's flag of token t0 + j
+template <int N>
 __device__ __forceinline__ bool reset_flag(const uint8_t* reset, int64_t row, int64_t t0, int64_t L, int lane) {
-    return lane < TPT && t0 + lane < L && reset[row * L + t0 + lane] != 0;
+    return lane < N && t0 + lane < L && reset[row * L + t0 + lane] != 0;
 }
 
 // the composition of a map with a state; a map with a restart inside forgets
@@ -235,11 +236,12 @@ struct Exchange {
     int abort;
 };
 
-// The ring of input tiles (64 rows of 64 channels): two rounds for bf16; one for
-// fp32, whose tiles are twice as large, so that three CTAs still share an SM.
-template <typename T> constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+// The forward's tokens per group: 8 (tiles of 64 rows) for bf16, 4 for fp32,
+// whose tiles are twice as large, so that three CTAs with two rounds of input
+// tiles each share an SM.
+template <typename T> constexpr int kFwdTokens = sizeof(T) == 2 ? 8 : 4;
 template <typename T> constexpr int kRowBytes = CPB * sizeof(T);
-template <typename T> constexpr int kTileBytes = TPT * kRowBytes<T>;
+template <typename T> constexpr int kTileBytes = TPT * kRowBytes<T>;  // a gradient warp's
 
 struct ScanMaps {
     CUtensorMap x, gate_a, gate_x, y;
@@ -249,7 +251,7 @@ template <typename T, bool RESET>
 __global__ void __launch_bounds__(kFwdThreads, 3)
     gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
-    constexpr int ST = kStages<T>, TB = kTileBytes<T>, CB = NW * TB;
+    constexpr int ST = 2, TPT = kFwdTokens<T>, TILE = NW * TPT, TB = TPT * kRowBytes<T>, CB = NW * TB;
     using Raw = typename Pair<T>::Raw;
     extern __shared__ __align__(128) uint8_t ring[];    // [ST][3] tiles: x, gate_x, gate_a (then y)
     __shared__ Exchange ex;
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
         const float2 k = decay_rates(p, c, active);
         const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
         int64_t t = first + warp * TPT;  // the group's first token
-        bool flag = RESET && reset_flag(p.reset, b, t, L, lane);
+        bool flag = RESET && reset_flag<TPT>(p.reset, b, t, L, lane);
         uint8_t* const mine = ring + warp * TB + lane * sizeof(Raw);
         for (int it = 0; it < rounds; ++it, t += round) {
             const int slot = it % ST;
@@ -378,7 +380,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
             uint32_t rst = 0;
             if constexpr (RESET) {
                 rst = __ballot_sync(0xffffffffu, flag);
-                flag = reset_flag(p.reset, b, t + round, L, lane);
+                flag = reset_flag<TPT>(p.reset, b, t + round, L, lane);
             }
             wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
             // the gates and the group's map
@@ -416,8 +418,8 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
             // bounded and it always arrives
             wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
             float2 h = ex.entering[warp][lane];
-            // a tile starts at a multiple of the interval: group 0 keeps its state
-            if (warp == 0 && p.states && active && t < L)
+            // (a kept state's token starts a group)
+            if (p.states && active && t < L && t % kInterval == 0)
                 *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
 #pragma unroll
             for (int j = 0; j < TPT; ++j) {
@@ -570,7 +572,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
     const float2 k = decay_rates(p, c, active);
     const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
     bool ok = true;
-    bool flag = RESET && reset_flag(p.reset, b, token(0), L, lane);
+    bool flag = RESET && reset_flag<TPT>(p.reset, b, token(0), L, lane);
     for (int it = 0; it < rounds; ++it) {
         const int64_t t = token(it);
         const int slot = it % ST;
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
         uint32_t rst = 0;
         if constexpr (RESET) {
             rst = __ballot_sync(0xffffffffu, flag);
-            flag = it + 1 < rounds && reset_flag(p.reset, b, t - round, L, lane);
+            flag = it + 1 < rounds && reset_flag<TPT>(p.reset, b, t - round, L, lane);
         }
         const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
         wait_phase(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
@@ -765,14 +767,14 @@ cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int threads, int64_
 constexpr int kMaxDevices = 64;
 template <typename Kern>
 int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern kern, int threads, size_t smem,
-                 int64_t blocks, int64_t batch, int64_t seqlen) {
+                 int64_t blocks, int64_t batch, int64_t tiles) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) {
         cudaGetLastError();
         return 1;
     }
     const double sms = device_sms();
-    const int64_t clusters = blocks * batch, tiles = (seqlen + TILE - 1) / TILE;
+    const int64_t clusters = blocks * batch;
     int best = 1;
     double least = 0.0;
     for (int cl = 1; cl <= kMaxCluster && cl <= tiles; ++cl) {
@@ -810,7 +812,8 @@ cudaError_t launch_clusters(Kern kern, int threads, const GatedScanParams& p, si
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.channels + CPB - 1) / CPB;
-    const int cl = cluster_size(held, kern, threads, smem, blocks, p.batch, p.seqlen);
+    constexpr int tile = NW * (BWD ? TPT : kFwdTokens<T>);
+    const int cl = cluster_size(held, kern, threads, smem, blocks, p.batch, (p.seqlen + tile - 1) / tile);
     *cluster = cl;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config(&attr, threads, blocks, p.batch, cl, smem, s);
@@ -824,12 +827,13 @@ size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
 }
 
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
-    const size_t smem = NW * kStages<T> * 3 * kTileBytes<T>;
+    constexpr int tile = NW * kFwdTokens<T>;
+    const size_t smem = 2 * 3 * tile * kRowBytes<T>;
     ScanMaps m;
     const std::pair<CUtensorMap*, const void*> arrays[] = {
         {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.y, p.y}};
     for (const auto& a : arrays)
-        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TILE))
+        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, tile))
             return cudaErrorInvalidValue;
     int cl = 1;
     return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, kFwdThreads, p, smem, s, &cl, m)
