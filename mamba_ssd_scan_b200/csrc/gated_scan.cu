@@ -31,8 +31,7 @@ namespace {
 
 constexpr int kInterval = SSD_GATED_SCAN_INTERVAL;
 constexpr int NW = 8;                   // groups per CTA, a warp each
-constexpr int kFwdThreads = (NW + 1) * 32;  // and the warp that composes their maps
-constexpr int kBwdThreads = NW * 32;
+constexpr int kThreads = (NW + 1) * 32;  // and the warp that moves tiles and composes maps
 constexpr int TPT = 8;           // the gradient's tokens per group
 constexpr int TILE = NW * TPT;   // and per CTA and round
 static_assert(TILE == kInterval, "a tile starts where a state is kept");
@@ -236,32 +235,7 @@ struct Exchange {
     int abort;
 };
 
-// The forward's tokens per group: 8 (tiles of 64 rows) for bf16, 4 for fp32,
-// whose tiles are twice as large, so that three CTAs with two rounds of input
-// tiles each share an SM.
-template <typename T> constexpr int kFwdTokens = sizeof(T) == 2 ? 8 : 4;
-template <typename T> constexpr int kRowBytes = CPB * sizeof(T);
-template <typename T> constexpr int kTileBytes = TPT * kRowBytes<T>;  // a gradient warp's
-
-struct ScanMaps {
-    CUtensorMap x, gate_a, gate_x, y;
-};
-
-template <typename T, bool RESET>
-__global__ void __launch_bounds__(kFwdThreads, 3)
-    gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
-    constexpr bool EXACT = sizeof(T) == 4;
-    constexpr int ST = 2, TPT = kFwdTokens<T>, TILE = NW * TPT, TB = TPT * kRowBytes<T>, CB = NW * TB;
-    using Raw = typename Pair<T>::Raw;
-    extern __shared__ __align__(128) uint8_t ring[];    // [ST][3] tiles: x, gate_x, gate_a (then y)
-    __shared__ Exchange ex;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
-    const int rank = static_cast<int>(blockIdx.x) % cl;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x / cl) * CPB, c = c0 + 2 * lane;
-    const bool active = c < C;
-    const int64_t round = static_cast<int64_t>(cl) * TILE;
-    const int rounds = static_cast<int>((L + round - 1) / round);
+template <typename E> __device__ __forceinline__ void init_exchange(E& ex) {
     if (threadIdx.x == 0) {
         tc::mbar_init(tc::smem_u32(&ex.maps_ready), NW);
         tc::mbar_init(tc::smem_u32(&ex.outputs_ready), NW);
@@ -275,6 +249,53 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
         ex.abort = 0;
     }
     __syncthreads();
+}
+
+// (one warp) This CTA's tile map m to every CTA of the cluster, and the wait for
+// all of theirs; false once it has given up.
+template <bool RESET, typename E>
+__device__ __forceinline__ bool exchange_tiles(E& ex, float4 m, bool rst, int it, int rank, int cl, bool withhold,
+                                               uint32_t tile_bytes, int lane) {
+    const int buf = it & 1;
+    const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
+    if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+    __syncwarp();
+    if (!withhold) {
+        for (int to = 0; to < cl; ++to)
+            store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
+        if (RESET && lane < cl)
+            store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst),
+                        in_rank(&ex.tiles_ready[buf], lane));
+    }
+    return __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, kPeerProbes, &ex.abort));
+}
+
+// The forward's tokens per group: 8 (tiles of 64 rows) for bf16, 4 for fp32,
+// whose tiles are twice as large, so that three CTAs with two rounds of input
+// tiles each share an SM.
+template <typename T> constexpr int kFwdTokens = sizeof(T) == 2 ? 8 : 4;
+template <typename T> constexpr int kRowBytes = CPB * sizeof(T);
+
+struct ScanMaps {
+    CUtensorMap x, gate_a, gate_x, y;
+};
+
+template <typename T, bool RESET>
+__global__ void __launch_bounds__(kThreads, 3)
+    gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
+    constexpr bool EXACT = sizeof(T) == 4;
+    constexpr int ST = 2, TPT = kFwdTokens<T>, TILE = NW * TPT, TB = TPT * kRowBytes<T>, CB = NW * TB;
+    using Raw = typename Pair<T>::Raw;
+    extern __shared__ __align__(128) uint8_t ring[];    // [ST][3] tiles: x, gate_x, gate_a (then y)
+    __shared__ Exchange ex;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
+    const int rank = static_cast<int>(blockIdx.x) % cl;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x / cl) * CPB, c = c0 + 2 * lane;
+    const bool active = c < C;
+    const int64_t round = static_cast<int64_t>(cl) * TILE;
+    const int rounds = static_cast<int>((L + round - 1) / round);
+    init_exchange(ex);
     if (cl > 1) cluster_sync_all();  // every CTA's barriers exist before a peer completes on them
     const int64_t first = static_cast<int64_t>(rank) * TILE;  // the tile's first token, round 0
 
@@ -327,16 +348,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
                     const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g[w].x, g[w].y), make_float2(m.x, m.y));
                     m = make_float4(aa.x, aa.y, hh.x, hh.y);
                 }
-                const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
-                if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
-                __syncwarp();
-                if (!(rank == 0 && it == withhold)) {
-                    for (int to = 0; to < cl; ++to)
-                        store_async(in_rank(&ex.tile_map[buf][rank][lane], to), m, in_rank(&ex.tiles_ready[buf], to));
-                    if (RESET && lane < cl)
-                        store_async(in_rank(&ex.tile_rst[buf][rank], lane), rst != 0, in_rank(&ex.tiles_ready[buf], lane));
-                }
-                ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, kPeerProbes, &ex.abort));
+                ok = exchange_tiles<RESET>(ex, m, rst != 0, it, rank, cl, rank == 0 && it == withhold, tile_bytes, lane);
                 for (int q = 0; q < cl; ++q) {
                     if (q == rank) h = carry;
                     carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -440,7 +452,7 @@ __global__ void __launch_bounds__(kFwdThreads, 3)
 // the map of the adjoint it passes on, c <- a (dy + c) token by token backwards,
 // whose factor is the same A.  The state entering a tile is the forward's (a
 // tile is one interval), so only the adjoint crosses tiles.  The warps form
-// both maps, warp 0 hands each group its entering state and adjoint, and the
+// both maps, the ninth hands each group its entering state and adjoint, and the
 // group is replayed, forwards for the states and backwards for the
 // outputs, which take the places of x, gate_x and gate_a in shared memory.
 struct ExchangeBwd {
@@ -449,10 +461,22 @@ struct ExchangeBwd {
     float4 tile_map[2][kMaxCluster][32];  // A, G of the cluster's tiles, two rounds
     float4 entering[NW][32];              // the state and the adjoint entering each group
     int group_rst[NW], tile_rst[2][kMaxCluster];
-    uint64_t maps_ready, states_ready, tiles_ready[2], loaded[NW][2];
+    uint64_t loaded[2], maps_ready, states_ready, outputs_ready, tiles_ready[2];
     int abort;
 };
 
+// A state is parked in the places of its token's gates, which are read by then.
+__device__ __forceinline__ void park(uint32_t* gx, uint32_t* ga, float2 h) {
+    *gx = __float_as_uint(h.x);
+    *ga = __float_as_uint(h.y);
+}
+__device__ __forceinline__ float2 unpark(const uint32_t* gx, const uint32_t* ga) {
+    return make_float2(__uint_as_float(*gx), __uint_as_float(*ga));
+}
+__device__ __forceinline__ void park(float2* gx, float2*, float2 h) { *gx = h; }
+__device__ __forceinline__ float2 unpark(const float2* gx, const float2*) { return *gx; }
+
+// rounds of input tiles in shared memory (one for fp32, so that two CTAs share an SM)
 template <typename T> constexpr int kStagesBwd = sizeof(T) == 2 ? 2 : 1;
 
 struct ScanBwdMaps {
@@ -460,12 +484,12 @@ struct ScanBwdMaps {
 };
 
 template <typename T, bool RESET>
-__global__ void __launch_bounds__(kBwdThreads, 2)
+__global__ void __launch_bounds__(kThreads, 2)
     gated_scan_bwd_kernel(GatedScanParams p, const __grid_constant__ ScanBwdMaps maps, int cl, int withhold) {
     constexpr bool EXACT = sizeof(T) == 4;
-    constexpr int ST = kStagesBwd<T>, TB = kTileBytes<T>;
+    constexpr int ST = kStagesBwd<T>, TB = TPT * kRowBytes<T>, CB = NW * TB;
     using Raw = typename Pair<T>::Raw;
-    extern __shared__ __align__(128) uint8_t ring[];    // [NW][ST][4] tiles: x, gate_x, gate_a, dy
+    extern __shared__ __align__(128) uint8_t ring[];    // [ST][4] tiles: x, gate_x, gate_a, dy; dx, dgate_x, dgate_a
     __shared__ ExchangeBwd ex;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
@@ -474,230 +498,207 @@ __global__ void __launch_bounds__(kBwdThreads, 2)
     const bool active = c < C;
     const int64_t round = static_cast<int64_t>(cl) * TILE;
     const int rounds = static_cast<int>((L + round - 1) / round);
-    if (threadIdx.x == 0) {
-        tc::mbar_init(tc::smem_u32(&ex.maps_ready), NW);
-        tc::mbar_init(tc::smem_u32(&ex.states_ready), 1);
-        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[0]), 1);
-        tc::mbar_init(tc::smem_u32(&ex.tiles_ready[1]), 1);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            tc::mbar_init(tc::smem_u32(&ex.loaded[w][0]), 1);
-            tc::mbar_init(tc::smem_u32(&ex.loaded[w][1]), 1);
-        }
-        tc::fence_mbar_init();
-        ex.abort = 0;
-    }
-    __syncthreads();
+    init_exchange(ex);
     if (cl > 1) cluster_sync_all();
+    // rounds run backwards: the first token of this CTA's tile
+    auto first = [&](int it) { return static_cast<int64_t>(rounds - 1 - it) * round + static_cast<int64_t>(rank) * TILE; };
     float2 sum = dup(0.0f);
 
-    // warp 0's part in a round, as in the forward
-    const int64_t nst = (L + kInterval - 1) / kInterval;
-    // the kept state entering this CTA's tile of a round (rounds run backwards)
-    auto kept = [&](int it) {
-        const int64_t tile = static_cast<int64_t>(rounds - 1 - it) * cl + rank;
-        return warp == 0 && active && it < rounds && tile < nst
-                   ? *reinterpret_cast<const float2*>(p.states + (b * nst + tile) * C + c)
-                   : dup(0.0f);
-    };
-    float2 carry = (warp == 0 && active && p.d_final) ? *reinterpret_cast<const float2*>(p.d_final + b * C + c) : dup(0.0f);
-    float2 next = kept(0);
-    const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
-    auto hand_out = [&](int it, bool ok) {
-        const int buf = it & 1;
-        float2 h = next;
-        next = kept(it + 1);
-        wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, kOwnProbes, &ex.abort);
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
-            h = apply(ex.group_map[w][lane], RESET && ex.group_rst[w], h);
-        }
-        auto factor = [&](int w) { return *reinterpret_cast<const float2*>(&ex.group_map[w][lane]); };
-        auto step = [&](int w, float2 v) {
-            const float2 G = ex.group_rev[w][lane];
-            return RESET && ex.group_rst[w] ? G : fma2(factor(w), v, G);
+    if (warp == NW) {
+        const uint32_t tiles = tc::smem_u32(ring);
+        const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
+        auto load = [&](int n) {
+            const uint32_t dst = tiles + (n % ST) * 4 * CB, bar = tc::smem_u32(&ex.loaded[n % ST]);
+            const int t = static_cast<int>(first(n));
+            tc::mbar_expect_tx(bar, 4 * CB);
+            tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
+            tc::tma_load_rows(dst + CB, &maps.gate_x, bar, ci, t, bi);
+            tc::tma_load_rows(dst + 2 * CB, &maps.gate_a, bar, ci, t, bi);
+            tc::tma_load_rows(dst + 3 * CB, &maps.dy, bar, ci, t, bi);
         };
-        float2 cin = carry;
-        if (cl > 1 && ok) {
-            float2 a = factor(NW - 1), g = ex.group_rev[NW - 1][lane];
-            bool rst = RESET && ex.group_rst[NW - 1];
+        if (lane == 0)
+            for (int n = 0; n < ST && n < rounds; ++n) load(n);
+        const int64_t nst = (L + kInterval - 1) / kInterval;
+        // the kept state entering this CTA's tile of a round
+        auto kept = [&](int it) {
+            const int64_t t = it < rounds ? first(it) : L;
+            return active && t < L ? *reinterpret_cast<const float2*>(p.states + (b * nst + t / kInterval) * C + c)
+                                   : dup(0.0f);
+        };
+        // the adjoint entering the round from the right
+        float2 carry = (active && p.d_final) ? *reinterpret_cast<const float2*>(p.d_final + b * C + c) : dup(0.0f);
+        float2 next = kept(0);
+        const uint32_t tile_bytes = static_cast<uint32_t>(cl) * (32 * sizeof(float4) + (RESET ? sizeof(int) : 0));
+        bool ok = true;
+        for (int it = 0; it < rounds; ++it) {
+            const int buf = it & 1;
+            float2 h = next;
+            next = kept(it + 1);
+            wait_phase(tc::smem_u32(&ex.maps_ready), it & 1, kOwnProbes, &ex.abort);
+            auto factor = [&](int w) { return *reinterpret_cast<const float2*>(&ex.group_map[w][lane]); };
+            auto step = [&](int w, float2 v) {
+                const float2 G = ex.group_rev[w][lane];
+                return RESET && ex.group_rst[w] ? G : fma2(factor(w), v, G);
+            };
+            float2 cin = carry;
+            if (cl > 1 && ok) {
+                float2 a = factor(NW - 1), g = ex.group_rev[NW - 1][lane];
+                bool rst = RESET && ex.group_rst[NW - 1];
 #pragma unroll
-            for (int w = NW - 2; w >= 0; --w) {
-                g = step(w, g);
-                a = RESET && ex.group_rst[w] ? dup(0.0f) : mul2(factor(w), a);
-                rst |= RESET && ex.group_rst[w];
+                for (int w = NW - 2; w >= 0; --w) {
+                    g = step(w, g);
+                    a = RESET && ex.group_rst[w] ? dup(0.0f) : mul2(factor(w), a);
+                    rst |= RESET && ex.group_rst[w];
+                }
+                ok = exchange_tiles<RESET>(ex, make_float4(a.x, a.y, g.x, g.y), rst, it, rank, cl,
+                                           rank == 0 && it == withhold, tile_bytes, lane);
+                for (int q = cl - 1; q >= 0; --q) {
+                    if (q == rank) cin = carry;
+                    carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
+                }
             }
-            const uint32_t bar = tc::smem_u32(&ex.tiles_ready[buf]);
-            if (lane == 0) tc::mbar_expect_tx(bar, tile_bytes);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                *reinterpret_cast<float2*>(&ex.entering[w][lane]) = h;
+                h = apply(ex.group_map[w][lane], RESET && ex.group_rst[w], h);
+            }
+#pragma unroll
+            for (int w = NW - 1; w >= 0; --w) {
+                *(reinterpret_cast<float2*>(&ex.entering[w][lane]) + 1) = cin;
+                cin = step(w, cin);
+            }
+            if (cl == 1) carry = cin;
             __syncwarp();
-            if (!(rank == 0 && it == withhold)) {
-                for (int to = 0; to < cl; ++to)
-                    store_async(in_rank(&ex.tile_map[buf][rank][lane], to), make_float4(a.x, a.y, g.x, g.y),
-                                in_rank(&ex.tiles_ready[buf], to));
-                if (RESET && lane < cl)
-                    store_async(in_rank(&ex.tile_rst[buf][rank], lane), static_cast<int>(rst), in_rank(&ex.tiles_ready[buf], lane));
-            }
-            ok = __all_sync(0xffffffffu, wait_phase(bar, (it >> 1) & 1, kPeerProbes, &ex.abort));
-            for (int q = cl - 1; q >= 0; --q) {
-                if (q == rank) cin = carry;
-                carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
+            wait_phase(tc::smem_u32(&ex.outputs_ready), it & 1, kOwnProbes, &ex.abort);
+            if (lane == 0) {
+                const int64_t t = first(it);
+                if (t < L) {
+                    const uint32_t out = tiles + (it % ST) * 4 * CB;
+                    tc::tma_store_rows(&maps.dx, out, ci, static_cast<int>(t), bi);
+                    tc::tma_store_rows(&maps.dgate_x, out + CB, ci, static_cast<int>(t), bi);
+                    tc::tma_store_rows(&maps.dgate_a, out + 2 * CB, ci, static_cast<int>(t), bi);
+                    tc::bulk_commit_group();
+                }
+                if (it + ST < rounds) {
+                    tc::bulk_wait_read_all();
+                    load(it + ST);
+                }
             }
         }
+        if (p.d_init && active && rank == 0) *reinterpret_cast<float2*>(p.d_init + b * C + c) = carry;
+        if (lane == 0) tc::bulk_wait_all();
+    } else {
+        const float2 k = decay_rates(p, c, active);
+        const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
+        bool flag = RESET && reset_flag<TPT>(p.reset, b, first(0) + warp * TPT, L, lane);
+        uint8_t* const mine = ring + warp * TB + lane * sizeof(Raw);
+        for (int it = 0; it < rounds; ++it) {
+            const int64_t t = first(it) + warp * TPT;
+            const int slot = it % ST;
+            uint8_t* src = mine + slot * 4 * CB;
+            auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * CB + j * kRowBytes<T>); };
+            uint32_t rst = 0;
+            if constexpr (RESET) {
+                rst = __ballot_sync(0xffffffffu, flag);
+                flag = it + 1 < rounds && reset_flag<TPT>(p.reset, b, t - round, L, lane);
+            }
+            const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
+            wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
+            float2 r[TPT], i[TPT], em1[TPT];
+            float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
+            auto form = [&](auto is_slow) {
 #pragma unroll
-        for (int w = NW - 1; w >= 0; --w) {
-            *(reinterpret_cast<float2*>(&ex.entering[w][lane]) + 1) = cin;
-            cin = step(w, cin);
-        }
-        if (cl == 1) carry = cin;
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.states_ready));
-        return ok;
-    };
-    const int64_t first = static_cast<int64_t>(rank) * TILE + warp * TPT;
-    const uint32_t tiles = tc::smem_u32(ring) + warp * ST * 4 * TB;
-    const int ci = static_cast<int>(c0), bi = static_cast<int>(b);
-    auto token = [&](int it) { return first + static_cast<int64_t>(rounds - 1 - it) * round; };
-    auto load = [&](int n) {
-        const uint32_t dst = tiles + (n % ST) * 4 * TB, bar = tc::smem_u32(&ex.loaded[warp][n % ST]);
-        const int t = static_cast<int>(token(n));
-        tc::mbar_expect_tx(bar, 4 * TB);
-        tc::tma_load_rows(dst, &maps.x, bar, ci, t, bi);
-        tc::tma_load_rows(dst + TB, &maps.gate_x, bar, ci, t, bi);
-        tc::tma_load_rows(dst + 2 * TB, &maps.gate_a, bar, ci, t, bi);
-        tc::tma_load_rows(dst + 3 * TB, &maps.dy, bar, ci, t, bi);
-    };
-    if (lane == 0)
-        for (int n = 0; n < ST && n < rounds; ++n) load(n);
-    const float2 k = decay_rates(p, c, active);
-    const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-    bool ok = true;
-    bool flag = RESET && reset_flag<TPT>(p.reset, b, token(0), L, lane);
-    for (int it = 0; it < rounds; ++it) {
-        const int64_t t = token(it);
-        const int slot = it % ST;
-        uint8_t* src = ring + (warp * ST + slot) * 4 * TB + lane * sizeof(Raw);
-        auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * TB + j * kRowBytes<T>); };
-        uint32_t rst = 0;
-        if constexpr (RESET) {
-            rst = __ballot_sync(0xffffffffu, flag);
-            flag = it + 1 < rounds && reset_flag<TPT>(p.reset, b, t - round, L, lane);
-        }
-        const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
-        wait_phase(tc::smem_u32(&ex.loaded[warp][slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
-        float2 r[TPT], i[TPT], em1[TPT];
-        float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
-        auto form = [&](auto is_slow) {
+                for (int j = 0; j < TPT; ++j) {
+                    float2 a;
+                    sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
+                    decays<EXACT, decltype(is_slow)::value>(mul2(k, r[j]), em1[j], a);
+                    float2 n = input_weight(em1[j]);
+                    const bool rs = RESET && ((rst >> j) & 1);
+                    if (rs) n = dup(1.0f);
+                    float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+                    if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
+                    A = rs ? dup(0.0f) : fma2(em1[j], A, A);
+                    H = rs ? u : add2(H, fma2(em1[j], H, u));
+                }
+            };
+            if (slow) form(std::true_type());
+            else form(std::false_type());
+#pragma unroll
+            for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
+                G = add2(G, Pair<T>::widen(*at(3, j)));
+                G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
+            }
+            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+            ex.group_rev[warp][lane] = G;
+            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+            wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
+            const float4 in = ex.entering[warp][lane];
+            float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
+            // What follows is formed again from r, i and em1: kept over the wait, n and u
+            // of the group would cost 32 more registers.
+#pragma unroll
+            for (int j = 0; j < TPT; ++j)
+                asm volatile("" : "+f"(em1[j].x), "+f"(em1[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
+            // forwards: the state before each token
 #pragma unroll
             for (int j = 0; j < TPT; ++j) {
-                float2 a;
-                sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
-                decays<EXACT, decltype(is_slow)::value>(mul2(k, r[j]), em1[j], a);
-            }
-        };
-        if (slow) form(std::true_type());
-        else form(std::false_type());
-#pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            float2 n = input_weight(em1[j]);
-            const bool rs = RESET && ((rst >> j) & 1);
-            if (rs) n = dup(1.0f);
-            float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-            if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
-            if (rs) {
-                A = dup(0.0f);
-                H = u;
-            } else {
-                A = fma2(em1[j], A, A);
-                H = add2(H, fma2(em1[j], H, u));
-            }
-        }
-#pragma unroll
-        for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
-            G = add2(G, Pair<T>::widen(*at(3, j)));
-            G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
-        }
-        ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-        ex.group_rev[warp][lane] = G;
-        if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-            if (ST == 2 && it > 0 && it + 1 < rounds) {
-                tc::bulk_wait_read_all();  // the previous round's outputs have left
-                load(it + 1);
-            }
-        }
-        if (warp == 0) ok = hand_out(it, ok);
-        else wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
-        const float4 in = ex.entering[warp][lane];
-        float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
-        float2 hp[TPT];
-#pragma unroll
-        for (int j = 0; j < TPT; ++j) {
-            hp[j] = h;
-            const bool rs = RESET && ((rst >> j) & 1);
-            const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
-            const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-            h = rs ? u : add2(h, fma2(em1[j], h, u));
-        }
-        auto back = [&](auto is_slow) {
-#pragma unroll
-            for (int j = TPT - 1; j >= 0; --j) {
+                park(at(1, j), at(2, j), h);
                 const bool rs = RESET && ((rst >> j) & 1);
-                const float2 x = Pair<T>::widen(*at(0, j));
-                g = add2(g, Pair<T>::widen(*at(3, j)));
-                const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
-                float2 a = add2(em1[j], dup(1.0f));
-                if constexpr (!decltype(is_slow)::value) {  // a small decay as it is, not as 1 + em1
-                    const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-                    a = make_float2(la.x >= -0.25f ? a.x : e.x, la.y >= -0.25f ? a.y : e.y);
+                const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
+                const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+                h = rs ? u : add2(h, fma2(em1[j], h, u));
+            }
+            // backwards: the outputs
+            auto back = [&](auto is_slow) {
+#pragma unroll
+                for (int j = TPT - 1; j >= 0; --j) {
+                    const bool rs = RESET && ((rst >> j) & 1);
+                    const float2 x = Pair<T>::widen(*at(0, j)), hp = unpark(at(1, j), at(2, j));
+                    g = add2(g, Pair<T>::widen(*at(3, j)));
+                    const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
+                    float2 a = add2(em1[j], dup(1.0f));
+                    if constexpr (!decltype(is_slow)::value) {  // a small decay as it is, not as 1 + em1
+                        const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
+                        a = make_float2(la.x >= -0.25f ? a.x : e.x, la.y >= -0.25f ? a.y : e.y);
+                    }
+                    // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
+                    // gives a finite dla, times la = 0
+                    const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
+                    const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)),
+                                                  rsqrt_approx(max_nan(n2.y, 1e-36f)));
+                    const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
+                    const float2 dx = mul2(mul2(g, n), i[j]);
+                    const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
+                    float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp));
+                    if (rs) dla = dup(0.0f);
+                    const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
+                    if (j < left) sum = fma2(dla, r[j], sum);
+                    g = rs ? dup(0.0f) : fma2(em1[j], g, g);
+                    *at(0, j) = Pair<T>::narrow(dx);
+                    *at(1, j) = Pair<T>::narrow(dgx);
+                    *at(2, j) = Pair<T>::narrow(dga);
+                    // two tokens at a time: all eight at once spill (388 us instead of 226)
+                    if ((j & 1) == 0) asm volatile("" ::: "memory");
                 }
-                // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
-                // gives a finite dla, times la = 0
-                const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
-                const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)), rsqrt_approx(max_nan(n2.y, 1e-36f)));
-                const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
-                const float2 dx = mul2(mul2(g, n), i[j]);
-                const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));
-                float2 dla = mul2(mul2(g, a), fma2(mul2(a, rn), mul2(ix, dup(-1.0f)), hp[j]));
-                if (rs) dla = dup(0.0f);
-                const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
-                if (j < left) sum = fma2(dla, r[j], sum);
-                g = rs ? dup(0.0f) : fma2(em1[j], g, g);
-                *at(0, j) = Pair<T>::narrow(dx);
-                *at(1, j) = Pair<T>::narrow(dgx);
-                *at(2, j) = Pair<T>::narrow(dga);
-            }
-        };
-        if (slow) back(std::true_type());
-        else back(std::false_type());
-        tc::fence_smem_async();
-        __syncwarp();
-        if (lane == 0) {
-            if (left > 0) {
-                const uint32_t out = tiles + slot * 4 * TB;
-                tc::tma_store_rows(&maps.dx, out, ci, static_cast<int>(t), bi);
-                tc::tma_store_rows(&maps.dgate_x, out + TB, ci, static_cast<int>(t), bi);
-                tc::tma_store_rows(&maps.dgate_a, out + 2 * TB, ci, static_cast<int>(t), bi);
-                tc::bulk_commit_group();
-            }
-            if (ST == 1 && it + 1 < rounds) {
-                tc::bulk_wait_read_all();
-                load(it + 1);
-            }
+            };
+            if (slow) back(std::true_type());
+            else back(std::false_type());
+            tc::fence_smem_async();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
         }
     }
-    if (lane == 0) tc::bulk_wait_all();
-    if (p.d_init && active && rank == 0 && warp == 0) *reinterpret_cast<float2*>(p.d_init + b * C + c) = carry;
     // the CTA's sums of dla r, group after group
     __syncthreads();
-    *reinterpret_cast<float2*>(&ex.entering[warp][lane]) = sum;
+    if (warp < NW) ex.group_rev[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && active) {
         float2 s = dup(0.0f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) s = add2(s, *reinterpret_cast<float2*>(&ex.entering[w][lane]));
+        for (int w = 0; w < NW; ++w) s = add2(s, ex.group_rev[w][lane]);
         *reinterpret_cast<float2*>(p.partial + (b * cl + rank) * C + c) = s;
     }
     if (cl > 1) cluster_sync_all();
@@ -743,11 +744,11 @@ int device_sms() {
     return n;
 }
 
-cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int threads, int64_t blocks, int64_t batch, int cl,
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int64_t blocks, int64_t batch, int cl,
                                   size_t smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks * cl), static_cast<unsigned>(batch));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     attr->id = cudaLaunchAttributeClusterDimension;
@@ -766,7 +767,7 @@ cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int threads, int64_
 // 256 us; 10, 281 us; 8, 345 us.  b8 L4096 C2048: 1, 145 us; 2, 158 us.)
 constexpr int kMaxDevices = 64;
 template <typename Kern>
-int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern kern, int threads, size_t smem,
+int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern kern, size_t smem,
                  int64_t blocks, int64_t batch, int64_t tiles) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) {
@@ -781,7 +782,7 @@ int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern ke
         int n = held[dev][cl].load(std::memory_order_relaxed);  // clusters at once; 0 = not asked, -1 = none
         if (n == 0) {
             cudaLaunchAttribute attr;
-            cudaLaunchConfig_t cfg = cluster_config(&attr, threads, 1, 1, cl, smem, nullptr);
+            cudaLaunchConfig_t cfg = cluster_config(&attr, 1, 1, cl, smem, nullptr);
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
                 cudaGetLastError();
@@ -804,7 +805,7 @@ int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern ke
 
 // T, BWD: one table of held clusters per kernel family.
 template <typename T, bool BWD, typename Kern, typename... Args>
-cudaError_t launch_clusters(Kern kern, int threads, const GatedScanParams& p, size_t smem, cudaStream_t s,
+cudaError_t launch_clusters(Kern kern, const GatedScanParams& p, size_t smem, cudaStream_t s,
                             int* cluster, const Args&... args) {
     static std::atomic<int> held[kMaxDevices][kMaxCluster + 1];
     // (attributes are the device's own: set on every call)
@@ -813,10 +814,10 @@ cudaError_t launch_clusters(Kern kern, int threads, const GatedScanParams& p, si
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.channels + CPB - 1) / CPB;
     constexpr int tile = NW * (BWD ? TPT : kFwdTokens<T>);
-    const int cl = cluster_size(held, kern, threads, smem, blocks, p.batch, (p.seqlen + tile - 1) / tile);
+    const int cl = cluster_size(held, kern, smem, blocks, p.batch, (p.seqlen + tile - 1) / tile);
     *cluster = cl;
     cudaLaunchAttribute attr;
-    const cudaLaunchConfig_t cfg = cluster_config(&attr, threads, blocks, p.batch, cl, smem, s);
+    const cudaLaunchConfig_t cfg = cluster_config(&attr, blocks, p.batch, cl, smem, s);
     return cudaLaunchKernelEx(&cfg, kern, p, args..., cl, static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP)));
 }
 
@@ -836,23 +837,23 @@ template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cu
         if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, tile))
             return cudaErrorInvalidValue;
     int cl = 1;
-    return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, kFwdThreads, p, smem, s, &cl, m)
-                   : launch_clusters<T, false>(gated_scan_kernel<T, false>, kFwdThreads, p, smem, s, &cl, m);
+    return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, p, smem, s, &cl, m)
+                   : launch_clusters<T, false>(gated_scan_kernel<T, false>, p, smem, s, &cl, m);
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {
-    const size_t smem = NW * kStagesBwd<T> * 4 * kTileBytes<T>;
+    const size_t smem = kStagesBwd<T> * 4 * TILE * kRowBytes<T>;
     ScanBwdMaps m;
     const std::pair<CUtensorMap*, const void*> arrays[] = {
         {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.dy, p.dy},
         {&m.dx, p.dx}, {&m.dgate_a, p.dgate_a}, {&m.dgate_x, p.dgate_x}};
     for (const auto& a : arrays)
-        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TPT))
+        if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, TILE))
             return cudaErrorInvalidValue;
     int cl = 1;
     const cudaError_t e =
-        p.reset ? launch_clusters<T, true>(gated_scan_bwd_kernel<T, true>, kBwdThreads, p, smem, s, &cl, m)
-                : launch_clusters<T, true>(gated_scan_bwd_kernel<T, false>, kBwdThreads, p, smem, s, &cl, m);
+        p.reset ? launch_clusters<T, true>(gated_scan_bwd_kernel<T, true>, p, smem, s, &cl, m)
+                : launch_clusters<T, true>(gated_scan_bwd_kernel<T, false>, p, smem, s, &cl, m);
     if (e != cudaSuccess) return e;
     return launch_kernel(gated_scan_finish_kernel, dim3(static_cast<unsigned>((p.channels + 31) / 32)),
                          dim3(kColSumThreads), 0, s, true, p, p.batch * cl);
