@@ -42,21 +42,29 @@ template <int N> __device__ __forceinline__ Slot slot_of(int l, int headdim, int
 }
 
 // cos and sin of position * inv_freq for a tile of tokens, in the order the
-// lanes read them: a slot's N pairs are N / 2 16-byte chunks of (cos, sin) x 2,
-// chunk k of slot l of token t at ((t * N / 2) + k) * rs + l.  The angle is an
-// fp64 product (positions up to 2^53 are exact; at 2^31 the turn is off by
-// less than 1e-7), reduced by whole turns before the fp32 cosine and sine.
-template <int N>
-__device__ void fill_angles(float2* cs, const NormRopeParams& p, int64_t tok0, int ntok) {
-    const int half = p.rot_dim / 2, rs = p.rot_dim / (2 * N);
-    for (int e = threadIdx.x; e < ntok * half; e += blockDim.x) {
-        const int t = e / half, j = e - t * half;
-        const int64_t tok = tok0 + t;
-        const int64_t pos = p.positions ? p.positions[tok] : tok % p.seqlen;
-        const double turns = static_cast<double>(pos) * static_cast<double>(p.inv_freq[j]) *
-                             0.15915494309189533577;  // 1 / (2 pi)
-        float sn, cn;
-        sincospif(2.0f * static_cast<float>(turns - rint(turns)), &sn, &cn);
+// lanes read them: a slot's N pairs are N / 2 16-byte chunks (c0, c1, s0, s1),
+// chunk k of slot l of token t at ((t * N / 2) + k) * rs + l.  A thread keeps one
+// pair j and steps through the tokens.  Its turns per position, inv_freq /
+// (2 pi), are held as a 64-bit fraction of a turn (formed in fp64), so the angle
+// is an integer product that drops the whole turns by itself: off by less than
+// 2^-25 of a turn at positions up to 2^31.
+template <int N> struct Angles {
+    int t0, tstep, place;  // first token, tokens per step (0: no pair), float offset of the pair in a token's chunks
+    int64_t turn;          // the fraction of a turn per position, times 2^64
+    __device__ __forceinline__ void init(const NormRopeParams& p) {
+        const int half = p.rot_dim / 2, rs = p.rot_dim / (2 * N);
+        t0 = tstep = place = 0;
+        turn = 0;
+        if (half == 0) return;
+        tstep = TPB / half;  // (half <= 128)
+        t0 = static_cast<int>(threadIdx.x) / half;
+        const int j = static_cast<int>(threadIdx.x) - t0 * half;
+        if (t0 >= tstep) {
+            tstep = 0;
+            return;
+        }
+        const double f = static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;  // 1 / (2 pi)
+        turn = static_cast<int64_t>((f - rint(f)) * 18446744073709549568.0);  // just below 2^64: no overflow at 1/2
         int l, w;  // the slot that holds pair j and its place there
         if (!p.adjacent) {
             l = j / N;
@@ -66,43 +74,58 @@ __device__ void fill_angles(float2* cs, const NormRopeParams& p, int64_t tok0, i
             l = jj / (N / 2);
             w = jj % (N / 2) + (j < q ? 0 : N / 2);
         }
-        cs[(((t * (N / 2)) + w / 2) * rs + l) * 2 + (w & 1)] = make_float2(cn, sn);
+        place = ((w / 2) * rs + l) * 4 + (w & 1);
     }
-}
+    __device__ __forceinline__ void fill(float4* cs, const NormRopeParams& p, int64_t tok0, int ntok) const {
+        if (tstep == 0) return;
+        const uint32_t len = static_cast<uint32_t>(p.seqlen);
+        for (int t = t0; t < ntok; t += tstep) {
+            const int64_t pos = p.positions ? p.positions[tok0 + t]
+                                            : static_cast<int64_t>(static_cast<uint32_t>(tok0 + t) % len);
+            const int64_t part = static_cast<int64_t>(static_cast<uint64_t>(pos) * static_cast<uint64_t>(turn));
+            float sn, cn;
+            sincospif(static_cast<float>(static_cast<int32_t>(part >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+            float* c = reinterpret_cast<float*>(cs) + t * p.rot_dim + place;
+            c[0] = cn;
+            c[2] = sn;
+        }
+    }
+};
 
-// Rotates a slot's N pairs: lo / hi are its two vectors.  `sign` -1 rotates back.
-template <int N>
-__device__ __forceinline__ void rotate(float* lo, float* hi, const float2* cs, int rs, int t, int l,
-                                       bool adjacent, float sign) {
-    const float4* c4 = reinterpret_cast<const float4*>(cs) + (t * (N / 2)) * rs + l;
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// Rotates a slot's N pairs by the angle (BACK: by its negative); lo / hi are its
+// two vectors as pairs of elements.
+template <int N, bool ADJ, bool BACK>
+__device__ __forceinline__ void rotate(float2 (&lo)[N / 2], float2 (&hi)[N / 2], const float4* c4, int rs) {
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) {
-        const float4 c = c4[k * rs];
-        const float s0 = sign * c.y, s1 = sign * c.w;
-        if (!adjacent) {
-            const float a0 = lo[2 * k], b0 = hi[2 * k], a1 = lo[2 * k + 1], b1 = hi[2 * k + 1];
-            lo[2 * k] = fmaf(a0, c.x, -b0 * s0);
-            hi[2 * k] = fmaf(a0, s0, b0 * c.x);
-            lo[2 * k + 1] = fmaf(a1, c.z, -b1 * s1);
-            hi[2 * k + 1] = fmaf(a1, s1, b1 * c.z);
-        } else {
-            float* v = (k < N / 4) ? lo + 4 * k : hi + 4 * (k - N / 4);
-            const float a0 = v[0], b0 = v[1], a1 = v[2], b1 = v[3];
-            v[0] = fmaf(a0, c.x, -b0 * s0);
-            v[1] = fmaf(a0, s0, b0 * c.x);
-            v[2] = fmaf(a1, c.z, -b1 * s1);
-            v[3] = fmaf(a1, s1, b1 * c.z);
+        const float4 v = c4[k * rs];
+        const float2 c = make_float2(v.x, v.y);
+        const float2 s = BACK ? make_float2(-v.z, -v.w) : make_float2(v.z, v.w);
+        if (!ADJ) {
+            const float2 a = lo[k], b = hi[k];
+            lo[k] = fma2(a, c, mul2(b, make_float2(-s.x, -s.y)));
+            hi[k] = fma2(a, s, mul2(b, c));
+        } else {  // chunk k: the pairs 2 k and 2 k + 1 of the slot
+            float2* q = (k < N / 4) ? lo + 2 * k : hi + 2 * (k - N / 4);
+            const float2 x = q[0], y = q[1];
+            q[0] = make_float2(fmaf(x.x, c.x, -x.y * s.x), fmaf(x.x, s.x, x.y * c.x));
+            q[1] = make_float2(fmaf(y.x, c.y, -y.y * s.y), fmaf(y.x, s.y, y.y * c.y));
         }
     }
 }
 
 template <int N>
-__device__ __forceinline__ void load_weight(const float* w, int v, float* o) {
+__device__ __forceinline__ void load_weight(const float* w, int v, float2 (&o)[N / 2]) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4) {
-        const float4 a = (w && v >= 0) ? __ldg(reinterpret_cast<const float4*>(w + v * N + i))
+    for (int i = 0; i < N / 4; ++i) {
+        const float4 a = (w && v >= 0) ? __ldg(reinterpret_cast<const float4*>(w + v * N) + i)
                                        : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-        o[i] = a.x; o[i + 1] = a.y; o[i + 2] = a.z; o[i + 3] = a.w;
+        o[2 * i] = make_float2(a.x, a.y);
+        o[2 * i + 1] = make_float2(a.z, a.w);
     }
 }
 
@@ -110,125 +133,196 @@ template <typename T>
 __device__ __forceinline__ uint4 load16(const T* p, int v) {
     return v >= 0 ? *reinterpret_cast<const uint4*>(p + v * Vec16<T>::N) : make_uint4(0, 0, 0, 0);
 }
+template <typename T> __device__ __forceinline__ void widen2(uint4 raw, float2 (&v)[Vec16<T>::N / 2]) {
+    Vec16<T>::widen(raw, reinterpret_cast<float*>(v));
+}
+template <typename T> __device__ __forceinline__ void store16(T* p, int v, const float2 (&x)[Vec16<T>::N / 2]) {
+    if (v >= 0) *reinterpret_cast<uint4*>(p + v * Vec16<T>::N) = Vec16<T>::narrow(reinterpret_cast<const float*>(x));
+}
 
+// A lane's place among the units of a tile of tokens: unit u is head u % heads
+// of token u / heads; the lane steps by the CTA's units without dividing again.
+struct Place {
+    int t, h, dt, dh, heads;
+    __device__ __forceinline__ void start(int u, int step, int n) {
+        heads = n;
+        t = u / n;
+        h = u - t * n;
+        dt = step / n;
+        dh = step - dt * n;
+    }
+    __device__ __forceinline__ void next() {
+        t += dt;
+        h += dh;
+        if (h >= heads) {
+            h -= heads;
+            ++t;
+        }
+    }
+};
 
-template <typename T>
-__global__ void __launch_bounds__(TPB) norm_rope_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens) {
+// The forward: a tile's units are its heads of q, then those of k.  A lane
+// loads its next unit before it works on the present one.
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens) {
     constexpr int N = Vec16<T>::N;
-    extern __shared__ __align__(16) float2 cs[];
+    extern __shared__ __align__(16) float4 cs[];
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tile;
     const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
-    fill_angles<N>(cs, p, tok0, ntok);
-    __syncthreads();
-    const int l = threadIdx.x & (lpu - 1);
-    const int step = TPB / lpu;
+    const int l = threadIdx.x & (lpu - 1), step = TPB / lpu;
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
     const int nq = ntok * p.heads[0], units = nq + ntok * p.heads[1];
-    // whole warps run the same number of rounds (the shuffles take all lanes)
-    for (int u0 = 0; u0 < units; u0 += step) {
-        const int u = u0 + static_cast<int>(threadIdx.x) / lpu;
-        const bool live = u < units;
-        const int kind = u < nq ? 0 : 1;
-        const int uu = live ? (kind ? u - nq : u) : 0;
-        const int heads = live && kind ? p.heads[1] : p.heads[0];
-        const int kd = live ? kind : 0;
-        const int t = uu / heads, h = uu - t * heads;
-        const int64_t tok = tok0 + t;
-        const T* in = static_cast<const T*>(p.in[kd]) + tok * p.in_stride[kd] + static_cast<int64_t>(h) * p.headdim;
-        float lo[N], hi[N], w0[N], w1[N];
-        Vec16<T>::widen(load16(in, live ? s.v0 : -1), lo);
-        Vec16<T>::widen(load16(in, live ? s.v1 : -1), hi);
-        load_weight<N>(p.weight[kd], s.v0, w0);
-        load_weight<N>(p.weight[kd], s.v1, w1);
-        float ss = 0.0f;
-#pragma unroll
-        for (int i = 0; i < N; ++i) ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
-        for (int o = lpu / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            lo[i] *= inv * w0[i];
-            hi[i] *= inv * w1[i];
+    int u = static_cast<int>(threadIdx.x) / lpu, kd = 0;
+    Place at;
+    at.start(u, step, p.heads[0]);
+    // the lane's place of unit u (past the last unit: nothing is loaded or stored)
+    auto settle = [&]() {
+        if (kd == 0 && u >= nq && u < units) {
+            kd = 1;
+            at.start(u - nq, step, p.heads[1]);
         }
-        if (s.rot) rotate<N>(lo, hi, cs, rs, t, l, p.adjacent, 1.0f);
+    };
+    auto in_at = [&]() {
+        return static_cast<const T*>(p.in[kd]) + (tok0 + at.t) * p.in_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
+    };
+    settle();
+    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
+    if (u < units) {
+        r0 = load16(in_at(), s.v0);
+        r1 = load16(in_at(), s.v1);
+    }
+    float2 w0[N / 2], w1[N / 2];
+    int loaded = -1;
+    Angles<N> angles;
+    angles.init(p);
+    angles.fill(cs, p, tok0, ntok);
+    __syncthreads();
+    // whole warps run the same number of rounds (the shuffles take all lanes)
+    const int rounds = (units + step - 1) / step;
+    for (int i = 0; i < rounds; ++i) {
+        const bool live = u < units;
+        const int t = live ? at.t : 0;
+        T* out = static_cast<T*>(p.out[kd]) + (tok0 + at.t) * p.out_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
+        if (loaded != kd) {
+            load_weight<N>(p.weight[kd], s.v0, w0);
+            load_weight<N>(p.weight[kd], s.v1, w1);
+            loaded = kd;
+        }
+        float2 lo[N / 2], hi[N / 2];
+        widen2<T>(r0, lo);
+        widen2<T>(r1, hi);
+        u += step;
+        at.next();
+        settle();
+        if (u < units) {
+            r0 = load16(in_at(), s.v0);
+            r1 = load16(in_at(), s.v1);
+        }
+        float2 ss = dup(0.0f);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) ss = fma2(lo[j], lo[j], fma2(hi[j], hi[j], ss));
+        float sum = ss.x + ss.y;
+        for (int o = lpu / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float2 inv = dup(rsqrtf(fmaf(sum, inv_d, p.eps)));
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            lo[j] = mul2(mul2(lo[j], inv), w0[j]);
+            hi[j] = mul2(mul2(hi[j], inv), w1[j]);
+        }
+        if (s.rot) rotate<N, ADJ, false>(lo, hi, cs + (t * (N / 2)) * rs + l, rs);
         if (live) {
-            T* out = static_cast<T*>(p.out[kd]) + tok * p.out_stride[kd] + static_cast<int64_t>(h) * p.headdim;
-            if (s.v0 >= 0) *reinterpret_cast<uint4*>(out + s.v0 * N) = Vec16<T>::narrow(lo);
-            if (s.v1 >= 0) *reinterpret_cast<uint4*>(out + s.v1 * N) = Vec16<T>::narrow(hi);
+            store16<T>(out, s.v0, lo);
+            store16<T>(out, s.v1, hi);
         }
     }
 }
 
-// The gradient of q (kind 0) or k (kind 1): a CTA takes tiles tile0, tile0 +
-// ctas, ... and leaves one row of the weight's gradient in partial.
-template <typename T>
-__global__ void __launch_bounds__(TPB) norm_rope_bwd_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens,
-                                                            int ctas_q) {
+// The gradient of q (kind 0) or k (kind 1): a CTA takes tiles cta, cta + ctas,
+// ... (their angles in two buffers by turns: one barrier per tile) and leaves
+// one row of the weight's gradient in partial.
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(TPB, 2) norm_rope_bwd_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens,
+                                                               int ctas_q) {
     constexpr int N = Vec16<T>::N;
-    extern __shared__ __align__(16) float2 cs[];
+    extern __shared__ __align__(16) float4 cs[];
     const int kd = static_cast<int>(blockIdx.x) < ctas_q ? 0 : 1;
     const int cta = kd ? blockIdx.x - ctas_q : blockIdx.x;
     const int ctas = kd ? gridDim.x - ctas_q : ctas_q;
     const int heads = p.heads[kd];
-    const int l = threadIdx.x & (lpu - 1);
-    const int step = TPB / lpu;
+    const int l = threadIdx.x & (lpu - 1), step = TPB / lpu;
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
-    float w0[N], w1[N], acc0[N] = {}, acc1[N] = {};
+    float2 w0[N / 2], w1[N / 2], acc0[N / 2], acc1[N / 2];
     load_weight<N>(p.weight[kd], s.v0, w0);
     load_weight<N>(p.weight[kd], s.v1, w1);
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) acc0[j] = acc1[j] = dup(0.0f);
+    Angles<N> angles;
+    angles.init(p);
     const int64_t ntiles = (tokens + tile - 1) / tile;
-    for (int64_t ti = cta; ti < ntiles; ti += ctas) {
+    int buf = 0;
+    for (int64_t ti = cta; ti < ntiles; ti += ctas, buf ^= 1) {
         const int64_t tok0 = ti * tile;
         const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
-        __syncthreads();  // the previous tile's angles are read
-        fill_angles<N>(cs, p, tok0, ntok);
-        __syncthreads();
-        const int units = ntok * heads;
-        for (int u0 = 0; u0 < units; u0 += step) {
-            const int u = u0 + static_cast<int>(threadIdx.x) / lpu;
+        float4* mine = cs + buf * (tile * p.rot_dim / 4);
+        const int units = ntok * heads, rounds = (units + step - 1) / step;
+        int u = static_cast<int>(threadIdx.x) / lpu;
+        Place at;
+        at.start(u, step, heads);
+        uint4 r0, r1, q0, q1;
+        auto fetch = [&]() {
             const bool live = u < units;
-            const int uu = live ? u : 0;
-            const int t = uu / heads, h = uu - t * heads;
-            const int64_t tok = tok0 + t, ho = static_cast<int64_t>(h) * p.headdim;
+            const int64_t tok = tok0 + at.t, ho = static_cast<int64_t>(at.h) * p.headdim;
             const T* in = static_cast<const T*>(p.in[kd]) + tok * p.in_stride[kd] + ho;
             const T* de = static_cast<const T*>(p.dout[kd]) + tok * p.dout_stride[kd] + ho;
-            float lo[N], hi[N], e0[N], e1[N];
-            Vec16<T>::widen(load16(in, live ? s.v0 : -1), lo);
-            Vec16<T>::widen(load16(in, live ? s.v1 : -1), hi);
-            Vec16<T>::widen(load16(de, live ? s.v0 : -1), e0);
-            Vec16<T>::widen(load16(de, live ? s.v1 : -1), e1);
-            if (s.rot) rotate<N>(e0, e1, cs, rs, t, l, p.adjacent, -1.0f);
-            float ss = 0.0f, m = 0.0f;
+            r0 = load16(in, live ? s.v0 : -1);
+            r1 = load16(in, live ? s.v1 : -1);
+            q0 = load16(de, live ? s.v0 : -1);
+            q1 = load16(de, live ? s.v1 : -1);
+        };
+        fetch();
+        angles.fill(mine, p, tok0, ntok);
+        __syncthreads();
+        for (int i = 0; i < rounds; ++i) {
+            const bool live = u < units;
+            const int t = live ? at.t : 0;
+            T* out = static_cast<T*>(p.din[kd]) + (tok0 + at.t) * p.din_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
+            float2 lo[N / 2], hi[N / 2], e0[N / 2], e1[N / 2];
+            widen2<T>(r0, lo);
+            widen2<T>(r1, hi);
+            widen2<T>(q0, e0);
+            widen2<T>(q1, e1);
+            u += step;
+            at.next();
+            if (i + 1 < rounds) fetch();
+            if (s.rot) rotate<N, ADJ, true>(e0, e1, mine + (t * (N / 2)) * rs + l, rs);
+            float2 ss = dup(0.0f), mm = dup(0.0f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                ss = fmaf(lo[i], lo[i], fmaf(hi[i], hi[i], ss));
-                m = fmaf(e0[i] * w0[i], lo[i], fmaf(e1[i] * w1[i], hi[i], m));
+            for (int j = 0; j < N / 2; ++j) {
+                ss = fma2(lo[j], lo[j], fma2(hi[j], hi[j], ss));
+                mm = fma2(mul2(e0[j], w0[j]), lo[j], fma2(mul2(e1[j], w1[j]), hi[j], mm));
             }
+            float sum = ss.x + ss.y, m = mm.x + mm.y;
             for (int o = lpu / 2; o > 0; o >>= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 m += __shfl_xor_sync(0xffffffffu, m, o);
             }
-            const float inv = rsqrtf(fmaf(ss, inv_d, p.eps));
-            const float k = -inv * inv * m * inv_d;
-            float d0[N], d1[N];
+            const float s1 = rsqrtf(fmaf(sum, inv_d, p.eps));
+            const float2 inv = dup(s1), k = dup(-s1 * s1 * m * inv_d);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                d0[i] = inv * fmaf(lo[i], k, e0[i] * w0[i]);
-                d1[i] = inv * fmaf(hi[i], k, e1[i] * w1[i]);
+            for (int j = 0; j < N / 2; ++j) {  // (a lane without a unit holds zeros)
+                const float2 n0 = mul2(lo[j], inv), n1 = mul2(hi[j], inv);
+                acc0[j] = fma2(e0[j], n0, acc0[j]);
+                acc1[j] = fma2(e1[j], n1, acc1[j]);
+                e0[j] = fma2(n0, k, mul2(mul2(e0[j], w0[j]), inv));
+                e1[j] = fma2(n1, k, mul2(mul2(e1[j], w1[j]), inv));
             }
             if (live) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    acc0[i] = fmaf(e0[i], lo[i] * inv, acc0[i]);
-                    acc1[i] = fmaf(e1[i], hi[i] * inv, acc1[i]);
-                }
-                T* out = static_cast<T*>(p.din[kd]) + tok * p.din_stride[kd] + ho;
-                if (s.v0 >= 0) *reinterpret_cast<uint4*>(out + s.v0 * N) = Vec16<T>::narrow(d0);
-                if (s.v1 >= 0) *reinterpret_cast<uint4*>(out + s.v1 * N) = Vec16<T>::narrow(d1);
+                store16<T>(out, s.v0, e0);
+                store16<T>(out, s.v1, e1);
             }
         }
     }
@@ -238,16 +332,18 @@ __global__ void __launch_bounds__(TPB) norm_rope_bwd_kernel(NormRopeParams p, in
     __shared__ float red[TPB / 32][256];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+    for (int j = 0; j < N / 2; ++j)
         for (int o = lpu; o < 32; o <<= 1) {
-            acc0[i] += __shfl_xor_sync(0xffffffffu, acc0[i], o);
-            acc1[i] += __shfl_xor_sync(0xffffffffu, acc1[i], o);
+            acc0[j].x += __shfl_xor_sync(0xffffffffu, acc0[j].x, o);
+            acc0[j].y += __shfl_xor_sync(0xffffffffu, acc0[j].y, o);
+            acc1[j].x += __shfl_xor_sync(0xffffffffu, acc1[j].x, o);
+            acc1[j].y += __shfl_xor_sync(0xffffffffu, acc1[j].y, o);
         }
     if (lane < lpu) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (s.v0 >= 0) red[warp][s.v0 * N + i] = acc0[i];
-            if (s.v1 >= 0) red[warp][s.v1 * N + i] = acc1[i];
+        for (int j = 0; j < N / 2; ++j) {
+            if (s.v0 >= 0) *reinterpret_cast<float2*>(&red[warp][s.v0 * N + 2 * j]) = acc0[j];
+            if (s.v1 >= 0) *reinterpret_cast<float2*>(&red[warp][s.v1 * N + 2 * j]) = acc1[j];
         }
     }
     __syncthreads();
@@ -296,7 +392,7 @@ int tile_tokens(int64_t tokens, int heads, int lpu, int rot_dim, int64_t ctas) {
     return static_cast<int>(t < 1 ? 1 : t);
 }
 
-constexpr int64_t kBwdCtas = 592;  // the backward's persistent CTAs, four per SM
+constexpr int64_t kBwdCtas = 296;  // the backward's persistent CTAs, two per SM
 
 }  // namespace
 
@@ -308,7 +404,8 @@ template <typename T> cudaError_t launch_norm_rope(const NormRopeParams& p, cuda
     const int lpu = lanes_per_unit(N, p.headdim, p.rot_dim);
     const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], lpu, p.rot_dim, 2 * device_sms());
     const size_t smem = static_cast<size_t>(tile) * p.rot_dim * 4;
-    norm_rope_kernel<T><<<static_cast<unsigned>((tokens + tile - 1) / tile), TPB, smem, s>>>(p, lpu, tile, tokens);
+    const auto kern = p.adjacent ? norm_rope_kernel<T, true> : norm_rope_kernel<T, false>;
+    kern<<<static_cast<unsigned>((tokens + tile - 1) / tile), TPB, smem, s>>>(p, lpu, tile, tokens);
     return cudaGetLastError();
 }
 
@@ -317,7 +414,7 @@ template <typename T> cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, 
     const int64_t tokens = p.batch * p.seqlen;
     const int lpu = lanes_per_unit(N, p.headdim, p.rot_dim);
     const int H = p.heads[0] + p.heads[1];
-    const int tile = tile_tokens(tokens, p.heads[0], lpu, p.rot_dim, 2 * device_sms());
+    const int tile = tile_tokens(tokens, p.heads[0], lpu, 2 * p.rot_dim, 2 * device_sms());
     const int64_t ntiles = (tokens + tile - 1) / tile;
     // the CTAs are shared out between q and k by their heads
     int64_t cq = kBwdCtas * p.heads[0] / H, ck = kBwdCtas - cq;
@@ -326,9 +423,9 @@ template <typename T> cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, 
     if (ck < 1) ck = 1;
     if (ck > ntiles) ck = ntiles;
     if (p.heads[1] == 0) ck = 0;
-    const size_t smem = static_cast<size_t>(tile) * p.rot_dim * 4;
-    norm_rope_bwd_kernel<T><<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, lpu, tile, tokens,
-                                                                            static_cast<int>(cq));
+    const size_t smem = 2 * static_cast<size_t>(tile) * p.rot_dim * 4;
+    const auto kern = p.adjacent ? norm_rope_bwd_kernel<T, true> : norm_rope_bwd_kernel<T, false>;
+    kern<<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, lpu, tile, tokens, static_cast<int>(cq));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
     return launch_kernel(norm_rope_finish_kernel,
