@@ -100,33 +100,50 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a
 // two vectors as pairs of elements.
 template <int N, bool ADJ, bool BACK>
 __device__ __forceinline__ void rotate(float2 (&lo)[N / 2], float2 (&hi)[N / 2], const float4* c4, int rs) {
+    const float2 neg = dup(-1.0f);
 #pragma unroll
     for (int k = 0; k < N / 2; ++k) {
         const float4 v = c4[k * rs];
-        const float2 c = make_float2(v.x, v.y);
-        const float2 s = BACK ? make_float2(-v.z, -v.w) : make_float2(v.z, v.w);
+        const float2 c = make_float2(v.x, v.y), s = make_float2(v.z, v.w);
         if (!ADJ) {
             const float2 a = lo[k], b = hi[k];
-            lo[k] = fma2(a, c, mul2(b, make_float2(-s.x, -s.y)));
-            hi[k] = fma2(a, s, mul2(b, c));
+            if (!BACK) {
+                lo[k] = fma2(mul2(b, s), neg, mul2(a, c));
+                hi[k] = fma2(a, s, mul2(b, c));
+            } else {
+                lo[k] = fma2(b, s, mul2(a, c));
+                hi[k] = fma2(mul2(a, s), neg, mul2(b, c));
+            }
         } else {  // chunk k: the pairs 2 k and 2 k + 1 of the slot
             float2* q = (k < N / 4) ? lo + 2 * k : hi + 2 * (k - N / 4);
             const float2 x = q[0], y = q[1];
-            q[0] = make_float2(fmaf(x.x, c.x, -x.y * s.x), fmaf(x.x, s.x, x.y * c.x));
-            q[1] = make_float2(fmaf(y.x, c.y, -y.y * s.y), fmaf(y.x, s.y, y.y * c.y));
+            const float s0 = BACK ? -s.x : s.x, s1 = BACK ? -s.y : s.y;
+            q[0] = make_float2(fmaf(x.x, c.x, -x.y * s0), fmaf(x.x, s0, x.y * c.x));
+            q[1] = make_float2(fmaf(y.x, c.y, -y.y * s1), fmaf(y.x, s1, y.y * c.y));
         }
     }
 }
 
-template <int N>
-__device__ __forceinline__ void load_weight(const float* w, int v, float2 (&o)[N / 2]) {
-#pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-        const float4 a = (w && v >= 0) ? __ldg(reinterpret_cast<const float4*>(w + v * N) + i)
-                                       : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
-        o[2 * i] = make_float2(a.x, a.y);
-        o[2 * i + 1] = make_float2(a.z, a.w);
+// The weights of q and k in the order the lanes read them: chunk k (a float4) of
+// slot l of kind kd at (kd * N / 2 + k) * LPU + l, the first N / 4 chunks of its
+// first vector, then those of its second; 1 without weights or elements.
+template <int N, int LPU>
+__device__ __forceinline__ void fill_weights(float4* ws, const NormRopeParams& p, int kd0, int kds) {
+    for (int e = threadIdx.x; e < kds * (N / 2) * LPU; e += TPB) {
+        const int l = e % LPU, k = e / LPU % (N / 2), kd = kd0 + e / LPU / (N / 2);
+        const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
+        const int v = k < N / 4 ? s.v0 : s.v1;
+        const float* w = p.weight[kd];
+        ws[e] = w && v >= 0 ? __ldg(reinterpret_cast<const float4*>(w + v * N) + k % (N / 4))
+                            : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
     }
+}
+// pair j of a slot's first (hi = 0) or second vector
+template <int N, int LPU>
+__device__ __forceinline__ void weight2(const float4* ws, int hi, int k, float2& a, float2& b) {
+    const float4 w = ws[(hi * (N / 4) + k) * LPU];
+    a = make_float2(w.x, w.y);
+    b = make_float2(w.z, w.w);
 }
 
 template <typename T>
@@ -141,123 +158,155 @@ template <typename T> __device__ __forceinline__ void store16(T* p, int v, const
 }
 
 // A lane's place among the units of a tile of tokens: unit u is head u % heads
-// of token u / heads; the lane steps by the CTA's units without dividing again.
+// of token u / heads; the lane steps by the CTA's units, and the element offset
+// of its unit with it, without dividing or multiplying again.
 struct Place {
     int t, h, dt, dh, heads;
-    __device__ __forceinline__ void start(int u, int step, int n) {
+    int64_t off, step_off, wrap_off;
+    __device__ __forceinline__ void start(int u, int step, int n, int64_t tok0, int64_t stride, int headdim) {
         heads = n;
         t = u / n;
         h = u - t * n;
         dt = step / n;
         dh = step - dt * n;
+        off = (tok0 + t) * stride + static_cast<int64_t>(h) * headdim;
+        step_off = dt * stride + static_cast<int64_t>(dh) * headdim;
+        wrap_off = stride - static_cast<int64_t>(n) * headdim;
     }
     __device__ __forceinline__ void next() {
         t += dt;
         h += dh;
+        off += step_off;
         if (h >= heads) {
             h -= heads;
             ++t;
+            off += wrap_off;
         }
     }
 };
 
-// The forward: a tile's units are its heads of q, then those of k.  A lane
-// loads its next unit before it works on the present one.
-template <typename T, bool ADJ>
-__global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens) {
-    constexpr int N = Vec16<T>::N;
+// The forward: a tile's units are its heads of q, then those of k.  A lane has
+// its next two units' loads in flight while it works on one.
+template <typename T, bool ADJ, int LPU>
+__global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int tile, int64_t tokens) {
+    constexpr int N = Vec16<T>::N, STEP = TPB / LPU;
     extern __shared__ __align__(16) float4 cs[];
+    __shared__ float4 ws[2 * (N / 2) * LPU];
     const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tile;
     const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
-    const int l = threadIdx.x & (lpu - 1), step = TPB / lpu;
+    const int l = threadIdx.x % LPU;
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
     const int nq = ntok * p.heads[0], units = nq + ntok * p.heads[1];
-    int u = static_cast<int>(threadIdx.x) / lpu, kd = 0;
-    Place at;
-    at.start(u, step, p.heads[0]);
-    // the lane's place of unit u (past the last unit: nothing is loaded or stored)
-    auto settle = [&]() {
-        if (kd == 0 && u >= nq && u < units) {
-            kd = 1;
-            at.start(u - nq, step, p.heads[1]);
+    // one place runs ahead with the loads, one follows with the stores
+    struct Walk {
+        Place at;
+        int u, kd;
+    };
+    auto settle = [&](Walk& w, const int64_t* strides) {
+        if (w.kd == 0 && w.u >= nq && w.u < units) {
+            w.kd = 1;
+            w.at.start(w.u - nq, STEP, p.heads[1], tok0, strides[1], p.headdim);
         }
     };
-    auto in_at = [&]() {
-        return static_cast<const T*>(p.in[kd]) + (tok0 + at.t) * p.in_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
+    auto begin = [&](Walk& w, const int64_t* strides) {
+        w.u = static_cast<int>(threadIdx.x) / LPU;
+        w.kd = 0;
+        w.at.start(w.u, STEP, p.heads[0], tok0, strides[0], p.headdim);
+        settle(w, strides);
     };
-    settle();
-    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0;
-    if (u < units) {
-        r0 = load16(in_at(), s.v0);
-        r1 = load16(in_at(), s.v1);
-    }
-    float2 w0[N / 2], w1[N / 2];
-    int loaded = -1;
+    auto advance = [&](Walk& w, const int64_t* strides) {
+        w.u += STEP;
+        w.at.next();
+        settle(w, strides);
+    };
+    Walk in, out;
+    begin(in, p.in_stride);
+    begin(out, p.out_stride);
+    uint4 r[2][2];
+    auto fetch = [&](int b) {
+        if (in.u < units) {
+            const T* v = static_cast<const T*>(in.kd ? p.in[1] : p.in[0]) + in.at.off;
+            r[b][0] = load16(v, s.v0);
+            r[b][1] = load16(v, s.v1);
+        } else {
+            r[b][0] = r[b][1] = make_uint4(0, 0, 0, 0);
+        }
+        advance(in, p.in_stride);
+    };
+    fetch(0);
+    fetch(1);
+    fill_weights<N, LPU>(ws, p, 0, 2);
     Angles<N> angles;
     angles.init(p);
     angles.fill(cs, p, tok0, ntok);
     __syncthreads();
-    // whole warps run the same number of rounds (the shuffles take all lanes)
-    const int rounds = (units + step - 1) / step;
-    for (int i = 0; i < rounds; ++i) {
-        const bool live = u < units;
-        const int t = live ? at.t : 0;
-        T* out = static_cast<T*>(p.out[kd]) + (tok0 + at.t) * p.out_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
-        if (loaded != kd) {
-            load_weight<N>(p.weight[kd], s.v0, w0);
-            load_weight<N>(p.weight[kd], s.v1, w1);
-            loaded = kd;
-        }
+    auto work = [&](int b) {
+        const bool live = out.u < units;
         float2 lo[N / 2], hi[N / 2];
-        widen2<T>(r0, lo);
-        widen2<T>(r1, hi);
-        u += step;
-        at.next();
-        settle();
-        if (u < units) {
-            r0 = load16(in_at(), s.v0);
-            r1 = load16(in_at(), s.v1);
-        }
-        float2 ss = dup(0.0f);
-#pragma unroll
-        for (int j = 0; j < N / 2; ++j) ss = fma2(lo[j], lo[j], fma2(hi[j], hi[j], ss));
-        float sum = ss.x + ss.y;
-        for (int o = lpu / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float2 inv = dup(rsqrtf(fmaf(sum, inv_d, p.eps)));
+        widen2<T>(r[b][0], lo);
+        widen2<T>(r[b][1], hi);
+        fetch(b);
+        float2 ss = dup(0.0f), s2 = ss;
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
-            lo[j] = mul2(mul2(lo[j], inv), w0[j]);
-            hi[j] = mul2(mul2(hi[j], inv), w1[j]);
+            ss = fma2(lo[j], lo[j], ss);
+            s2 = fma2(hi[j], hi[j], s2);
         }
-        if (s.rot) rotate<N, ADJ, false>(lo, hi, cs + (t * (N / 2)) * rs + l, rs);
+        float sum = (ss.x + ss.y) + (s2.x + s2.y);
+#pragma unroll
+        for (int o = LPU / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float2 inv = dup(rsqrtf(fmaf(sum, inv_d, p.eps)));
+        const float4* w = ws + (live ? out.kd : 0) * (N / 2) * LPU + l;
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            float2 a, c;
+            weight2<N, LPU>(w, 0, k, a, c);
+            lo[2 * k] = mul2(mul2(lo[2 * k], inv), a);
+            lo[2 * k + 1] = mul2(mul2(lo[2 * k + 1], inv), c);
+            weight2<N, LPU>(w, 1, k, a, c);
+            hi[2 * k] = mul2(mul2(hi[2 * k], inv), a);
+            hi[2 * k + 1] = mul2(mul2(hi[2 * k + 1], inv), c);
+        }
+        if (s.rot) rotate<N, ADJ, false>(lo, hi, cs + (live ? out.at.t : 0) * (p.rot_dim / 4) + l, rs);
         if (live) {
-            store16<T>(out, s.v0, lo);
-            store16<T>(out, s.v1, hi);
+            T* v = static_cast<T*>(out.kd ? p.out[1] : p.out[0]) + out.at.off;
+            store16<T>(v, s.v0, lo);
+            store16<T>(v, s.v1, hi);
         }
+        advance(out, p.out_stride);
+    };
+    // whole warps run the same number of rounds (the shuffles take all lanes)
+    const int rounds = (units + STEP - 1) / STEP;
+    for (int i = 0; i < rounds; i += 2) {
+        work(0);
+        if (i + 1 < rounds) work(1);
     }
 }
 
 // The gradient of q (kind 0) or k (kind 1): a CTA takes tiles cta, cta + ctas,
 // ... (their angles in two buffers by turns: one barrier per tile) and leaves
 // one row of the weight's gradient in partial.
-template <typename T, bool ADJ>
-__global__ void __launch_bounds__(TPB, 2) norm_rope_bwd_kernel(NormRopeParams p, int lpu, int tile, int64_t tokens,
-                                                               int ctas_q) {
-    constexpr int N = Vec16<T>::N;
+template <typename T, bool ADJ, int LPU>
+__global__ void __launch_bounds__(TPB, 2)
+    norm_rope_bwd_kernel(NormRopeParams p, int tile, int64_t tokens, int ctas_q) {
+    constexpr int N = Vec16<T>::N, STEP = TPB / LPU;
     extern __shared__ __align__(16) float4 cs[];
+    __shared__ float4 ws[(N / 2) * LPU];
     const int kd = static_cast<int>(blockIdx.x) < ctas_q ? 0 : 1;
     const int cta = kd ? blockIdx.x - ctas_q : blockIdx.x;
     const int ctas = kd ? gridDim.x - ctas_q : ctas_q;
     const int heads = p.heads[kd];
-    const int l = threadIdx.x & (lpu - 1), step = TPB / lpu;
+    const int l = threadIdx.x % LPU;
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
-    float2 w0[N / 2], w1[N / 2], acc0[N / 2], acc1[N / 2];
-    load_weight<N>(p.weight[kd], s.v0, w0);
-    load_weight<N>(p.weight[kd], s.v1, w1);
+    const T* const in = static_cast<const T*>(p.in[kd]);
+    const T* const dout = static_cast<const T*>(p.dout[kd]);
+    T* const din = static_cast<T*>(p.din[kd]);
+    fill_weights<N, LPU>(ws, p, kd, 1);
+    float2 acc0[N / 2], acc1[N / 2];
 #pragma unroll
     for (int j = 0; j < N / 2; ++j) acc0[j] = acc1[j] = dup(0.0f);
     Angles<N> angles;
@@ -268,45 +317,56 @@ __global__ void __launch_bounds__(TPB, 2) norm_rope_bwd_kernel(NormRopeParams p,
         const int64_t tok0 = ti * tile;
         const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
         float4* mine = cs + buf * (tile * p.rot_dim / 4);
-        const int units = ntok * heads, rounds = (units + step - 1) / step;
-        int u = static_cast<int>(threadIdx.x) / lpu;
-        Place at;
-        at.start(u, step, heads);
+        const int units = ntok * heads, rounds = (units + STEP - 1) / STEP;
+        const int u0 = static_cast<int>(threadIdx.x) / LPU;
+        Place iat, eat, oat;
+        iat.start(u0, STEP, heads, tok0, p.in_stride[kd], p.headdim);
+        eat.start(u0, STEP, heads, tok0, p.dout_stride[kd], p.headdim);
+        oat.start(u0, STEP, heads, tok0, p.din_stride[kd], p.headdim);
+        int fu = u0, u = u0;
         uint4 r0, r1, q0, q1;
         auto fetch = [&]() {
-            const bool live = u < units;
-            const int64_t tok = tok0 + at.t, ho = static_cast<int64_t>(at.h) * p.headdim;
-            const T* in = static_cast<const T*>(p.in[kd]) + tok * p.in_stride[kd] + ho;
-            const T* de = static_cast<const T*>(p.dout[kd]) + tok * p.dout_stride[kd] + ho;
-            r0 = load16(in, live ? s.v0 : -1);
-            r1 = load16(in, live ? s.v1 : -1);
-            q0 = load16(de, live ? s.v0 : -1);
-            q1 = load16(de, live ? s.v1 : -1);
+            const bool live = fu < units;
+            r0 = load16(in + iat.off, live ? s.v0 : -1);
+            r1 = load16(in + iat.off, live ? s.v1 : -1);
+            q0 = load16(dout + eat.off, live ? s.v0 : -1);
+            q1 = load16(dout + eat.off, live ? s.v1 : -1);
+            fu += STEP;
+            iat.next();
+            eat.next();
         };
         fetch();
         angles.fill(mine, p, tok0, ntok);
         __syncthreads();
-        for (int i = 0; i < rounds; ++i) {
+        for (int i = 0; i < rounds; ++i, u += STEP, oat.next()) {
             const bool live = u < units;
-            const int t = live ? at.t : 0;
-            T* out = static_cast<T*>(p.din[kd]) + (tok0 + at.t) * p.din_stride[kd] + static_cast<int64_t>(at.h) * p.headdim;
             float2 lo[N / 2], hi[N / 2], e0[N / 2], e1[N / 2];
             widen2<T>(r0, lo);
             widen2<T>(r1, hi);
             widen2<T>(q0, e0);
             widen2<T>(q1, e1);
-            u += step;
-            at.next();
             if (i + 1 < rounds) fetch();
-            if (s.rot) rotate<N, ADJ, true>(e0, e1, mine + (t * (N / 2)) * rs + l, rs);
-            float2 ss = dup(0.0f), mm = dup(0.0f);
+            if (s.rot) rotate<N, ADJ, true>(e0, e1, mine + (live ? oat.t : 0) * (p.rot_dim / 4) + l, rs);
+            // e w of both vectors, the sum of squares and of e w v
+            float2 ss = dup(0.0f), mm = ss, g0[N / 2], g1[N / 2];
+#pragma unroll
+            for (int k = 0; k < N / 4; ++k) {
+                float2 a, c;
+                weight2<N, LPU>(ws + l, 0, k, a, c);
+                g0[2 * k] = mul2(e0[2 * k], a);
+                g0[2 * k + 1] = mul2(e0[2 * k + 1], c);
+                weight2<N, LPU>(ws + l, 1, k, a, c);
+                g1[2 * k] = mul2(e1[2 * k], a);
+                g1[2 * k + 1] = mul2(e1[2 * k + 1], c);
+            }
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
                 ss = fma2(lo[j], lo[j], fma2(hi[j], hi[j], ss));
-                mm = fma2(mul2(e0[j], w0[j]), lo[j], fma2(mul2(e1[j], w1[j]), hi[j], mm));
+                mm = fma2(g0[j], lo[j], fma2(g1[j], hi[j], mm));
             }
             float sum = ss.x + ss.y, m = mm.x + mm.y;
-            for (int o = lpu / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int o = LPU / 2; o > 0; o >>= 1) {
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 m += __shfl_xor_sync(0xffffffffu, m, o);
             }
@@ -317,12 +377,12 @@ __global__ void __launch_bounds__(TPB, 2) norm_rope_bwd_kernel(NormRopeParams p,
                 const float2 n0 = mul2(lo[j], inv), n1 = mul2(hi[j], inv);
                 acc0[j] = fma2(e0[j], n0, acc0[j]);
                 acc1[j] = fma2(e1[j], n1, acc1[j]);
-                e0[j] = fma2(n0, k, mul2(mul2(e0[j], w0[j]), inv));
-                e1[j] = fma2(n1, k, mul2(mul2(e1[j], w1[j]), inv));
+                e0[j] = fma2(n0, k, mul2(g0[j], inv));
+                e1[j] = fma2(n1, k, mul2(g1[j], inv));
             }
             if (live) {
-                store16<T>(out, s.v0, e0);
-                store16<T>(out, s.v1, e1);
+                store16<T>(din + oat.off, s.v0, e0);
+                store16<T>(din + oat.off, s.v1, e1);
             }
         }
     }
@@ -333,13 +393,14 @@ __global__ void __launch_bounds__(TPB, 2) norm_rope_bwd_kernel(NormRopeParams p,
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < N / 2; ++j)
-        for (int o = lpu; o < 32; o <<= 1) {
+#pragma unroll
+        for (int o = LPU; o < 32; o <<= 1) {
             acc0[j].x += __shfl_xor_sync(0xffffffffu, acc0[j].x, o);
             acc0[j].y += __shfl_xor_sync(0xffffffffu, acc0[j].y, o);
             acc1[j].x += __shfl_xor_sync(0xffffffffu, acc1[j].x, o);
             acc1[j].y += __shfl_xor_sync(0xffffffffu, acc1[j].y, o);
         }
-    if (lane < lpu) {
+    if (lane < LPU) {
 #pragma unroll
         for (int j = 0; j < N / 2; ++j) {
             if (s.v0 >= 0) *reinterpret_cast<float2*>(&red[warp][s.v0 * N + 2 * j]) = acc0[j];
@@ -398,23 +459,21 @@ constexpr int64_t kBwdCtas = 296;  // the backward's persistent CTAs, two per SM
 
 int64_t norm_rope_bwd_rows() { return kBwdCtas; }
 
-template <typename T> cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s) {
-    constexpr int N = Vec16<T>::N;
+namespace {
+
+template <typename T, int LPU> cudaError_t launch_fwd(const NormRopeParams& p, cudaStream_t s) {
     const int64_t tokens = p.batch * p.seqlen;
-    const int lpu = lanes_per_unit(N, p.headdim, p.rot_dim);
-    const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], lpu, p.rot_dim, 2 * device_sms());
+    const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], LPU, p.rot_dim, 2 * device_sms());
     const size_t smem = static_cast<size_t>(tile) * p.rot_dim * 4;
-    const auto kern = p.adjacent ? norm_rope_kernel<T, true> : norm_rope_kernel<T, false>;
-    kern<<<static_cast<unsigned>((tokens + tile - 1) / tile), TPB, smem, s>>>(p, lpu, tile, tokens);
+    const auto kern = p.adjacent ? norm_rope_kernel<T, true, LPU> : norm_rope_kernel<T, false, LPU>;
+    kern<<<static_cast<unsigned>((tokens + tile - 1) / tile), TPB, smem, s>>>(p, tile, tokens);
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s) {
-    constexpr int N = Vec16<T>::N;
+template <typename T, int LPU> cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t s) {
     const int64_t tokens = p.batch * p.seqlen;
-    const int lpu = lanes_per_unit(N, p.headdim, p.rot_dim);
     const int H = p.heads[0] + p.heads[1];
-    const int tile = tile_tokens(tokens, p.heads[0], lpu, 2 * p.rot_dim, 2 * device_sms());
+    const int tile = tile_tokens(tokens, p.heads[0], LPU, 2 * p.rot_dim, 2 * device_sms());
     const int64_t ntiles = (tokens + tile - 1) / tile;
     // the CTAs are shared out between q and k by their heads
     int64_t cq = kBwdCtas * p.heads[0] / H, ck = kBwdCtas - cq;
@@ -424,13 +483,33 @@ template <typename T> cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, 
     if (ck > ntiles) ck = ntiles;
     if (p.heads[1] == 0) ck = 0;
     const size_t smem = 2 * static_cast<size_t>(tile) * p.rot_dim * 4;
-    const auto kern = p.adjacent ? norm_rope_bwd_kernel<T, true> : norm_rope_bwd_kernel<T, false>;
-    kern<<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, lpu, tile, tokens, static_cast<int>(cq));
+    const auto kern = p.adjacent ? norm_rope_bwd_kernel<T, true, LPU> : norm_rope_bwd_kernel<T, false, LPU>;
+    kern<<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, tile, tokens, static_cast<int>(cq));
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
     return launch_kernel(norm_rope_finish_kernel,
                          dim3(static_cast<unsigned>((p.headdim + 31) / 32), ck > 0 ? 2 : 1),
                          dim3(kColSumThreads), 0, s, true, p, cq, ck);
+}
+
+template <typename T, bool BWD> cudaError_t launch(const NormRopeParams& p, cudaStream_t s) {
+    switch (lanes_per_unit(Vec16<T>::N, p.headdim, p.rot_dim)) {
+        case 1: return BWD ? launch_bwd<T, 1>(p, s) : launch_fwd<T, 1>(p, s);
+        case 2: return BWD ? launch_bwd<T, 2>(p, s) : launch_fwd<T, 2>(p, s);
+        case 4: return BWD ? launch_bwd<T, 4>(p, s) : launch_fwd<T, 4>(p, s);
+        case 8: return BWD ? launch_bwd<T, 8>(p, s) : launch_fwd<T, 8>(p, s);
+        case 16: return BWD ? launch_bwd<T, 16>(p, s) : launch_fwd<T, 16>(p, s);
+        default: return BWD ? launch_bwd<T, 32>(p, s) : launch_fwd<T, 32>(p, s);
+    }
+}
+
+}  // namespace
+
+template <typename T> cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t s) {
+    return launch<T, false>(p, s);
+}
+template <typename T> cudaError_t launch_norm_rope_bwd(const NormRopeParams& p, cudaStream_t s) {
+    return launch<T, true>(p, s);
 }
 
 template cudaError_t launch_norm_rope<float>(const NormRopeParams&, cudaStream_t);
