@@ -622,7 +622,7 @@ ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* args, void*
  *   q_out may be q with the same stride (in place), k_out k likewise; nothing
  *   else may overlap.
  * Supported: headdim a multiple of 8, <= 256; rot_dim a multiple of 16, <=
- *   headdim; strides a multiple of 8 (bf16) or 4 (fp32) elements; q_heads >= 1,
+ *   headdim; strides a multiple of 8 (bf16) or 4 (fp32) elements, < 2^28; q_heads >= 1,
  *   k_heads >= 0; q_heads + k_heads <= 65536; batch * seqlen < 2^31 (else
  *   SSD_ERR_UNSUPPORTED); strides >= heads * headdim; eps >= 0 and finite;
  *   pointers 16-byte aligned (positions: 8) (else SSD_ERR_INVALID_ARG). */

@@ -312,13 +312,15 @@ template <typename Args> ssd_status check_qk_sizes(const Args* a) {
     return SSD_OK;
 }
 
+constexpr int64_t kMaxStride = int64_t{1} << 28;  // elements
+
 // Token strides {q, q', k, k'}: at least the dense heads, whole 16-byte vectors.
 ssd_status check_qk_strides(const int64_t* s, int64_t q_heads, int64_t k_heads, int64_t headdim, int dtype) {
     for (int i = 0; i < 4; ++i) {
         const int64_t heads = i < 2 ? q_heads : k_heads;
         if (heads == 0) continue;
         if (s[i] < heads * headdim) return SSD_ERR_INVALID_ARG;
-        if (s[i] % (dtype == SSD_BF16 ? 8 : 4) != 0 || s[i] > kMaxTokens) return SSD_ERR_UNSUPPORTED;
+        if (s[i] % (dtype == SSD_BF16 ? 8 : 4) != 0 || s[i] >= kMaxStride) return SSD_ERR_UNSUPPORTED;
     }
     return SSD_OK;
 }

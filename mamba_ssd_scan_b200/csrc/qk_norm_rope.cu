@@ -41,6 +41,28 @@ template <int N> __device__ __forceinline__ Slot slot_of(int l, int headdim, int
     return s;
 }
 
+__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// (cos, sin) of 2 pi f for a fraction of a turn f in [-1/2, 1/2): the nearest
+// quarter turn is taken off and the rest x, |x| <= pi / 4, goes through the two
+// Taylor series side by side, sin to x^9 and cos to x^8 (what they leave out is
+// below 2^-25).
+__device__ __forceinline__ float2 cos_sin_turn(float f) {
+    const float q = rintf(4.0f * f);
+    const float x = fmaf(q, -0.25f, f) * 6.283185307179586f, x2 = x * x;
+    const float2 y = dup(x2);
+    // (cos, sin / x)
+    float2 v = fma2(make_float2(1.0f / 40320.0f, 1.0f / 362880.0f), y, make_float2(-1.0f / 720.0f, -1.0f / 5040.0f));
+    v = fma2(v, y, make_float2(1.0f / 24.0f, 1.0f / 120.0f));
+    v = fma2(v, y, make_float2(-0.5f, -1.0f / 6.0f));
+    const float c = fmaf(v.x, x2, 1.0f), sn = fmaf(v.y * x2, x, x);
+    const int n = static_cast<int>(q);  // quarter turns, -2 .. 2
+    const float a = (n & 1) ? sn : c, b = (n & 1) ? c : sn;
+    return make_float2(((n + 1) & 2) ? -a : a, (n & 2) ? -b : b);
+}
+
 // cos and sin of position * inv_freq for a tile of tokens, in the order the
 // lanes read them: a slot's N pairs are N / 2 16-byte chunks (c0, c1, s0, s1),
 // chunk k of slot l of token t at ((t * N / 2) + k) * rs + l.  A thread keeps one
@@ -79,22 +101,19 @@ template <int N> struct Angles {
     __device__ __forceinline__ void fill(float4* cs, const NormRopeParams& p, int64_t tok0, int ntok) const {
         if (tstep == 0) return;
         const uint32_t len = static_cast<uint32_t>(p.seqlen);
+        uint32_t own = p.positions ? 0u : static_cast<uint32_t>(tok0 + t0) % len;  // the token's place in its row
         for (int t = t0; t < ntok; t += tstep) {
-            const int64_t pos = p.positions ? p.positions[tok0 + t]
-                                            : static_cast<int64_t>(static_cast<uint32_t>(tok0 + t) % len);
+            const int64_t pos = p.positions ? p.positions[tok0 + t] : static_cast<int64_t>(own);
+            own += tstep;
+            while (own >= len) own -= len;
             const int64_t part = static_cast<int64_t>(static_cast<uint64_t>(pos) * static_cast<uint64_t>(turn));
-            float sn, cn;
-            sincospif(static_cast<float>(static_cast<int32_t>(part >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+            const float2 v = cos_sin_turn(static_cast<float>(static_cast<int32_t>(part >> 32)) * 2.3283064365386963e-10f);
             float* c = reinterpret_cast<float*>(cs) + t * p.rot_dim + place;
-            c[0] = cn;
-            c[2] = sn;
+            c[0] = v.x;
+            c[2] = v.y;
         }
     }
 };
-
-__device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
 // Rotates a slot's N pairs by the angle (BACK: by its negative); lo / hi are its
 // two vectors as pairs of elements.
@@ -158,130 +177,119 @@ template <typename T> __device__ __forceinline__ void store16(T* p, int v, const
 }
 
 // A lane's place among the units of a tile of tokens: unit u is head u % heads
-// of token u / heads; the lane steps by the CTA's units, and the element offset
-// of its unit with it, without dividing or multiplying again.
+// of token u / heads, and a lane steps by the CTA's units (dt tokens and dh
+// heads) without dividing again.
 struct Place {
-    int t, h, dt, dh, heads;
-    int64_t off, step_off, wrap_off;
-    __device__ __forceinline__ void start(int u, int step, int n, int64_t tok0, int64_t stride, int headdim) {
-        heads = n;
-        t = u / n;
-        h = u - t * n;
-        dt = step / n;
-        dh = step - dt * n;
-        off = (tok0 + t) * stride + static_cast<int64_t>(h) * headdim;
-        step_off = dt * stride + static_cast<int64_t>(dh) * headdim;
-        wrap_off = stride - static_cast<int64_t>(n) * headdim;
-    }
-    __device__ __forceinline__ void next() {
+    int t, h;
+    __device__ __forceinline__ void next(int dt, int dh, int heads) {
         t += dt;
         h += dh;
-        off += step_off;
         if (h >= heads) {
             h -= heads;
             ++t;
-            off += wrap_off;
         }
     }
 };
+// the head at a place, from the tile's first token (strides fit 32 bits in bytes)
+template <typename T>
+__device__ __forceinline__ const T* head_at(const T* tile, const Place& w, int stride, int headdim) {
+    return tile + (static_cast<int64_t>(w.t) * stride + w.h * headdim);
+}
 
-// The forward: a tile's units are its heads of q, then those of k.  A lane has
-// its next two units' loads in flight while it works on one.
+// The forward.  A CTA takes tiles blockIdx.x, + gridDim.x, ... (their angles in
+// two buffers by turns: one barrier per tile); a tile's rounds go through the
+// heads of q, then those of k.  A lane has its next two units' loads in flight
+// while it works on one.
 template <typename T, bool ADJ, int LPU>
 __global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int tile, int64_t tokens) {
     constexpr int N = Vec16<T>::N, STEP = TPB / LPU;
     extern __shared__ __align__(16) float4 cs[];
     __shared__ float4 ws[2 * (N / 2) * LPU];
-    const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * tile;
-    const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
-    const int l = threadIdx.x % LPU;
+    const int l = threadIdx.x % LPU, u0 = static_cast<int>(threadIdx.x) / LPU;
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
-    const int nq = ntok * p.heads[0], units = nq + ntok * p.heads[1];
-    // one place runs ahead with the loads, one follows with the stores
-    struct Walk {
-        Place at;
-        int u, kd;
-    };
-    auto settle = [&](Walk& w, const int64_t* strides) {
-        if (w.kd == 0 && w.u >= nq && w.u < units) {
-            w.kd = 1;
-            w.at.start(w.u - nq, STEP, p.heads[1], tok0, strides[1], p.headdim);
-        }
-    };
-    auto begin = [&](Walk& w, const int64_t* strides) {
-        w.u = static_cast<int>(threadIdx.x) / LPU;
-        w.kd = 0;
-        w.at.start(w.u, STEP, p.heads[0], tok0, strides[0], p.headdim);
-        settle(w, strides);
-    };
-    auto advance = [&](Walk& w, const int64_t* strides) {
-        w.u += STEP;
-        w.at.next();
-        settle(w, strides);
-    };
-    Walk in, out;
-    begin(in, p.in_stride);
-    begin(out, p.out_stride);
-    uint4 r[2][2];
-    auto fetch = [&](int b) {
-        if (in.u < units) {
-            const T* v = static_cast<const T*>(in.kd ? p.in[1] : p.in[0]) + in.at.off;
-            r[b][0] = load16(v, s.v0);
-            r[b][1] = load16(v, s.v1);
-        } else {
-            r[b][0] = r[b][1] = make_uint4(0, 0, 0, 0);
-        }
-        advance(in, p.in_stride);
-    };
-    fetch(0);
-    fetch(1);
+    const int nq = p.heads[0], nk = p.heads[1];
+    const int dtq = STEP / nq, dhq = STEP - dtq * nq, dtk = nk ? STEP / nk : 0, dhk = STEP - dtk * nk;
+    // where the lane's first units lie in a tile
+    Place q0, k0;
+    q0.t = u0 / nq;
+    q0.h = u0 - q0.t * nq;
+    k0.t = nk ? u0 / nk : 0;
+    k0.h = u0 - k0.t * nk;
+    const int64_t ntiles = (tokens + tile - 1) / tile;
     fill_weights<N, LPU>(ws, p, 0, 2);
     Angles<N> angles;
     angles.init(p);
-    angles.fill(cs, p, tok0, ntok);
-    __syncthreads();
-    auto work = [&](int b) {
-        const bool live = out.u < units;
-        float2 lo[N / 2], hi[N / 2];
-        widen2<T>(r[b][0], lo);
-        widen2<T>(r[b][1], hi);
-        fetch(b);
-        float2 ss = dup(0.0f), s2 = ss;
+    int buf = 0;
+    for (int64_t ti = blockIdx.x; ti < ntiles; ti += gridDim.x, buf ^= 1) {
+        const int64_t tok0 = ti * tile;
+        const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
+        float4* mine = cs + buf * (tile * p.rot_dim / 4);
+        const int rq = (ntok * nq + STEP - 1) / STEP, rounds = rq + (ntok * nk + STEP - 1) / STEP;
+        const T* const qi = static_cast<const T*>(p.in[0]) + tok0 * p.in_stride[0];
+        const T* const ki = static_cast<const T*>(p.in[1]) + tok0 * p.in_stride[1];
+        T* const qo = static_cast<T*>(p.out[0]) + tok0 * p.out_stride[0];
+        T* const ko = static_cast<T*>(p.out[1]) + tok0 * p.out_stride[1];
+        int fi = 0;  // the round to load next, and its place
+        Place at = q0, held[2];
+        uint4 r[2][2];
+        auto fetch = [&](int b) {
+            if (fi == rq) at = k0;
+            const bool q = fi < rq, live = fi < rounds && at.t < ntok;
+            const T* v = q ? head_at(qi, at, static_cast<int>(p.in_stride[0]), p.headdim)
+                           : head_at(ki, at, static_cast<int>(p.in_stride[1]), p.headdim);
+            r[b][0] = load16(v, live ? s.v0 : -1);
+            r[b][1] = load16(v, live ? s.v1 : -1);
+            held[b] = at;
+            at.next(q ? dtq : dtk, q ? dhq : dhk, q ? nq : nk);
+            ++fi;
+        };
+        fetch(0);
+        fetch(1);
+        angles.fill(mine, p, tok0, ntok);
+        __syncthreads();
+        auto work = [&](int i, int b) {
+            const Place w = held[b];
+            const bool live = w.t < ntok;
+            float2 lo[N / 2], hi[N / 2];
+            widen2<T>(r[b][0], lo);
+            widen2<T>(r[b][1], hi);
+            fetch(b);
+            float2 ss = dup(0.0f), s2 = ss;
 #pragma unroll
-        for (int j = 0; j < N / 2; ++j) {
-            ss = fma2(lo[j], lo[j], ss);
-            s2 = fma2(hi[j], hi[j], s2);
-        }
-        float sum = (ss.x + ss.y) + (s2.x + s2.y);
+            for (int j = 0; j < N / 2; ++j) {
+                ss = fma2(lo[j], lo[j], ss);
+                s2 = fma2(hi[j], hi[j], s2);
+            }
+            float sum = (ss.x + ss.y) + (s2.x + s2.y);
 #pragma unroll
-        for (int o = LPU / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float2 inv = dup(rsqrtf(fmaf(sum, inv_d, p.eps)));
-        const float4* w = ws + (live ? out.kd : 0) * (N / 2) * LPU + l;
+            for (int o = LPU / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float2 inv = dup(rsqrtf(fmaf(sum, inv_d, p.eps)));
+            const float4* wt = ws + (i < rq ? 0 : (N / 2) * LPU) + l;
 #pragma unroll
-        for (int k = 0; k < N / 4; ++k) {
-            float2 a, c;
-            weight2<N, LPU>(w, 0, k, a, c);
-            lo[2 * k] = mul2(mul2(lo[2 * k], inv), a);
-            lo[2 * k + 1] = mul2(mul2(lo[2 * k + 1], inv), c);
-            weight2<N, LPU>(w, 1, k, a, c);
-            hi[2 * k] = mul2(mul2(hi[2 * k], inv), a);
-            hi[2 * k + 1] = mul2(mul2(hi[2 * k + 1], inv), c);
+            for (int k = 0; k < N / 4; ++k) {
+                float2 a, c;
+                weight2<N, LPU>(wt, 0, k, a, c);
+                lo[2 * k] = mul2(mul2(lo[2 * k], inv), a);
+                lo[2 * k + 1] = mul2(mul2(lo[2 * k + 1], inv), c);
+                weight2<N, LPU>(wt, 1, k, a, c);
+                hi[2 * k] = mul2(mul2(hi[2 * k], inv), a);
+                hi[2 * k + 1] = mul2(mul2(hi[2 * k + 1], inv), c);
+            }
+            if (s.rot) rotate<N, ADJ, false>(lo, hi, mine + (live ? w.t : 0) * (p.rot_dim / 4) + l, rs);
+            if (live) {
+                T* v = const_cast<T*>(i < rq ? head_at<T>(qo, w, static_cast<int>(p.out_stride[0]), p.headdim)
+                                             : head_at<T>(ko, w, static_cast<int>(p.out_stride[1]), p.headdim));
+                store16<T>(v, s.v0, lo);
+                store16<T>(v, s.v1, hi);
+            }
+        };
+        // (a round is the whole CTA's: its shuffles take all lanes)
+        for (int i = 0; i < rounds; i += 2) {
+            work(i, 0);
+            if (i + 1 < rounds) work(i + 1, 1);
         }
-        if (s.rot) rotate<N, ADJ, false>(lo, hi, cs + (live ? out.at.t : 0) * (p.rot_dim / 4) + l, rs);
-        if (live) {
-            T* v = static_cast<T*>(out.kd ? p.out[1] : p.out[0]) + out.at.off;
-            store16<T>(v, s.v0, lo);
-            store16<T>(v, s.v1, hi);
-        }
-        advance(out, p.out_stride);
-    };
-    // whole warps run the same number of rounds (the shuffles take all lanes)
-    const int rounds = (units + STEP - 1) / STEP;
-    for (int i = 0; i < rounds; i += 2) {
-        work(0);
-        if (i + 1 < rounds) work(1);
     }
 }
 
@@ -305,6 +313,13 @@ __global__ void __launch_bounds__(TPB, 2)
     const T* const in = static_cast<const T*>(p.in[kd]);
     const T* const dout = static_cast<const T*>(p.dout[kd]);
     T* const din = static_cast<T*>(p.din[kd]);
+    // where the lane's first unit lies in a tile
+    Place first;
+    first.t = static_cast<int>(threadIdx.x) / LPU / heads;
+    first.h = static_cast<int>(threadIdx.x) / LPU - first.t * heads;
+    const int dt = STEP / heads, dh = STEP - dt * heads;
+    const int is = static_cast<int>(p.in_stride[kd]), es = static_cast<int>(p.dout_stride[kd]);
+    const int os = static_cast<int>(p.din_stride[kd]);
     fill_weights<N, LPU>(ws, p, kd, 1);
     float2 acc0[N / 2], acc1[N / 2];
 #pragma unroll
@@ -317,36 +332,36 @@ __global__ void __launch_bounds__(TPB, 2)
         const int64_t tok0 = ti * tile;
         const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
         float4* mine = cs + buf * (tile * p.rot_dim / 4);
-        const int units = ntok * heads, rounds = (units + STEP - 1) / STEP;
-        const int u0 = static_cast<int>(threadIdx.x) / LPU;
-        Place iat, eat, oat;
-        iat.start(u0, STEP, heads, tok0, p.in_stride[kd], p.headdim);
-        eat.start(u0, STEP, heads, tok0, p.dout_stride[kd], p.headdim);
-        oat.start(u0, STEP, heads, tok0, p.din_stride[kd], p.headdim);
-        int fu = u0, u = u0;
+        const int rounds = (ntok * heads + STEP - 1) / STEP;
+        const T* const vi = in + tok0 * p.in_stride[kd];
+        const T* const ei = dout + tok0 * p.dout_stride[kd];
+        T* const vo = din + tok0 * p.din_stride[kd];
+        Place at = first, held;
         uint4 r0, r1, q0, q1;
         auto fetch = [&]() {
-            const bool live = fu < units;
-            r0 = load16(in + iat.off, live ? s.v0 : -1);
-            r1 = load16(in + iat.off, live ? s.v1 : -1);
-            q0 = load16(dout + eat.off, live ? s.v0 : -1);
-            q1 = load16(dout + eat.off, live ? s.v1 : -1);
-            fu += STEP;
-            iat.next();
-            eat.next();
+            const bool live = at.t < ntok;
+            const T* v = head_at(vi, at, is, p.headdim);
+            const T* e = head_at(ei, at, es, p.headdim);
+            r0 = load16(v, live ? s.v0 : -1);
+            r1 = load16(v, live ? s.v1 : -1);
+            q0 = load16(e, live ? s.v0 : -1);
+            q1 = load16(e, live ? s.v1 : -1);
+            held = at;
+            at.next(dt, dh, heads);
         };
         fetch();
         angles.fill(mine, p, tok0, ntok);
         __syncthreads();
-        for (int i = 0; i < rounds; ++i, u += STEP, oat.next()) {
-            const bool live = u < units;
+        for (int i = 0; i < rounds; ++i) {
+            const Place w = held;
+            const bool live = w.t < ntok;
             float2 lo[N / 2], hi[N / 2], e0[N / 2], e1[N / 2];
             widen2<T>(r0, lo);
             widen2<T>(r1, hi);
             widen2<T>(q0, e0);
             widen2<T>(q1, e1);
             if (i + 1 < rounds) fetch();
-            if (s.rot) rotate<N, ADJ, true>(e0, e1, mine + (live ? oat.t : 0) * (p.rot_dim / 4) + l, rs);
+            if (s.rot) rotate<N, ADJ, true>(e0, e1, mine + (live ? w.t : 0) * (p.rot_dim / 4) + l, rs);
             // e w of both vectors, the sum of squares and of e w v
             float2 ss = dup(0.0f), mm = ss, g0[N / 2], g1[N / 2];
 #pragma unroll
@@ -381,8 +396,9 @@ __global__ void __launch_bounds__(TPB, 2)
                 e1[j] = fma2(n1, k, mul2(g1[j], inv));
             }
             if (live) {
-                store16<T>(din + oat.off, s.v0, e0);
-                store16<T>(din + oat.off, s.v1, e1);
+                T* v = const_cast<T*>(head_at<T>(vo, w, os, p.headdim));
+                store16<T>(v, s.v0, e0);
+                store16<T>(v, s.v1, e1);
             }
         }
     }
@@ -443,13 +459,14 @@ int lanes_per_unit(int n, int headdim, int rot_dim) {
     return lpu;
 }
 
-// Tokens per CTA: enough for several rounds of units, few enough that the
-// grid fills the device and the angles fit 32 KB of shared memory.
+// Tokens per tile: about eight rounds of units, evened out so that the CTAs
+// (ctas at once) get the same number of tiles, and few enough that two tiles'
+// angles fit 64 KB of shared memory.
 int tile_tokens(int64_t tokens, int heads, int lpu, int rot_dim, int64_t ctas) {
-    int64_t t = (tokens + ctas - 1) / ctas;
-    const int64_t rounds = (static_cast<int64_t>(8) * (TPB / lpu) + heads - 1) / heads;  // 8 rounds
-    if (t > rounds) t = rounds;
+    int64_t t = (static_cast<int64_t>(8) * (TPB / lpu) + heads - 1) / heads;
     if (rot_dim > 0 && t > 32768 / (rot_dim * 4)) t = 32768 / (rot_dim * 4);
+    const int64_t turns = (tokens + ctas * t - 1) / (ctas * t);
+    t = (tokens + ctas * turns - 1) / (ctas * turns);
     return static_cast<int>(t < 1 ? 1 : t);
 }
 
@@ -461,31 +478,40 @@ int64_t norm_rope_bwd_rows() { return kBwdCtas; }
 
 namespace {
 
+// (dynamic shared memory beyond 48 KB is asked for: two tiles' angles can take 64 KB)
+template <typename Kern> cudaError_t allow_smem(Kern kern) {
+    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+}
+
 template <typename T, int LPU> cudaError_t launch_fwd(const NormRopeParams& p, cudaStream_t s) {
-    const int64_t tokens = p.batch * p.seqlen;
-    const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], LPU, p.rot_dim, 2 * device_sms());
-    const size_t smem = static_cast<size_t>(tile) * p.rot_dim * 4;
+    const int64_t tokens = p.batch * p.seqlen, slots = 3 * device_sms();
+    const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], LPU, p.rot_dim, slots);
+    const int64_t ntiles = (tokens + tile - 1) / tile, grid = ntiles < slots ? ntiles : slots;
     const auto kern = p.adjacent ? norm_rope_kernel<T, true, LPU> : norm_rope_kernel<T, false, LPU>;
-    kern<<<static_cast<unsigned>((tokens + tile - 1) / tile), TPB, smem, s>>>(p, tile, tokens);
+    const cudaError_t e = allow_smem(kern);
+    if (e != cudaSuccess) return e;
+    kern<<<static_cast<unsigned>(grid), TPB, 2 * static_cast<size_t>(tile) * p.rot_dim * 4, s>>>(p, tile, tokens);
     return cudaGetLastError();
 }
 
 template <typename T, int LPU> cudaError_t launch_bwd(const NormRopeParams& p, cudaStream_t s) {
     const int64_t tokens = p.batch * p.seqlen;
     const int H = p.heads[0] + p.heads[1];
-    const int tile = tile_tokens(tokens, p.heads[0], LPU, 2 * p.rot_dim, 2 * device_sms());
-    const int64_t ntiles = (tokens + tile - 1) / tile;
     // the CTAs are shared out between q and k by their heads
     int64_t cq = kBwdCtas * p.heads[0] / H, ck = kBwdCtas - cq;
     if (cq < 1) cq = 1;
+    const int tile = tile_tokens(tokens, p.heads[0], LPU, p.rot_dim, cq);
+    const int64_t ntiles = (tokens + tile - 1) / tile;
     if (cq > ntiles) cq = ntiles;
     if (ck < 1) ck = 1;
     if (ck > ntiles) ck = ntiles;
     if (p.heads[1] == 0) ck = 0;
     const size_t smem = 2 * static_cast<size_t>(tile) * p.rot_dim * 4;
     const auto kern = p.adjacent ? norm_rope_bwd_kernel<T, true, LPU> : norm_rope_bwd_kernel<T, false, LPU>;
+    cudaError_t e = allow_smem(kern);
+    if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, tile, tokens, static_cast<int>(cq));
-    const cudaError_t e = cudaGetLastError();
+    e = cudaGetLastError();
     if (e != cudaSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
     return launch_kernel(norm_rope_finish_kernel,
                          dim3(static_cast<unsigned>((p.headdim + 31) / 32), ck > 0 ? 2 : 1),
