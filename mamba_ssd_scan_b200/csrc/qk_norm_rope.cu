@@ -165,15 +165,35 @@ __device__ __forceinline__ void weight2(const float4* ws, int hi, int k, float2&
     b = make_float2(w.z, w.w);
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 load16(const T* p, int v) {
-    return v >= 0 ? *reinterpret_cast<const uint4*>(p + v * Vec16<T>::N) : make_uint4(0, 0, 0, 0);
-}
 template <typename T> __device__ __forceinline__ void widen2(uint4 raw, float2 (&v)[Vec16<T>::N / 2]) {
     Vec16<T>::widen(raw, reinterpret_cast<float*>(v));
 }
-template <typename T> __device__ __forceinline__ void store16(T* p, int v, const float2 (&x)[Vec16<T>::N / 2]) {
-    if (v >= 0) *reinterpret_cast<uint4*>(p + v * Vec16<T>::N) = Vec16<T>::narrow(reinterpret_cast<const float*>(x));
+template <typename T> __device__ __forceinline__ uint4 narrow2(const float2 (&x)[Vec16<T>::N / 2]) {
+    return Vec16<T>::narrow(reinterpret_cast<const float*>(x));
+}
+
+// What a lane needs to reach its slot of a head: the byte offset of its first
+// vector (in the base pointers), from there to its second, and which it has.
+struct Reach {
+    int first, delta;
+    bool has0, has1;
+};
+template <int N> __device__ __forceinline__ Reach reach_of(const Slot& s) {
+    Reach r;
+    r.has0 = s.v0 >= 0;
+    r.has1 = s.v1 >= 0;
+    r.first = r.has0 ? s.v0 * 16 : 0;
+    r.delta = r.has1 ? s.v1 * 16 - r.first : 0;
+    return r;
+}
+// (a vector that is not loaded keeps what the registers held)
+__device__ __forceinline__ void load_slot(const char* v, bool live, const Reach& x, uint4& a, uint4& b) {
+    if (live && x.has0) a = *reinterpret_cast<const uint4*>(v);
+    if (live && x.has1) b = *reinterpret_cast<const uint4*>(v + x.delta);
+}
+__device__ __forceinline__ void store_slot(char* v, bool live, const Reach& x, uint4 a, uint4 b) {
+    if (live && x.has0) *reinterpret_cast<uint4*>(v) = a;
+    if (live && x.has1) *reinterpret_cast<uint4*>(v + x.delta) = b;
 }
 
 // A lane's place among the units of a tile of tokens: unit u is head u % heads
@@ -190,10 +210,10 @@ struct Place {
         }
     }
 };
-// the head at a place, from the tile's first token (strides fit 32 bits in bytes)
-template <typename T>
-__device__ __forceinline__ const T* head_at(const T* tile, const Place& w, int stride, int headdim) {
-    return tile + (static_cast<int64_t>(w.t) * stride + w.h * headdim);
+// the byte offset of a place's head from the tile's first token (a token's
+// stride fits 32 bits)
+__device__ __forceinline__ int64_t head_at(const Place& w, int stride, int head) {
+    return static_cast<int64_t>(w.t) * stride + w.h * head;
 }
 
 // The forward.  A CTA takes tiles blockIdx.x, + gridDim.x, ... (their angles in
@@ -217,7 +237,14 @@ __global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int
     q0.h = u0 - q0.t * nq;
     k0.t = nk ? u0 / nk : 0;
     k0.h = u0 - k0.t * nk;
+    const Reach x = reach_of<N>(s);
+    constexpr int E = sizeof(T);
+    const int head = p.headdim * E;  // bytes, as the strides
+    const int qis = static_cast<int>(p.in_stride[0]) * E, kis = static_cast<int>(p.in_stride[1]) * E;
+    const int qos = static_cast<int>(p.out_stride[0]) * E, kos = static_cast<int>(p.out_stride[1]) * E;
     const int64_t ntiles = (tokens + tile - 1) / tile;
+    uint4 r[2][2];
+    r[0][0] = r[0][1] = r[1][0] = r[1][1] = make_uint4(0, 0, 0, 0);
     fill_weights<N, LPU>(ws, p, 0, 2);
     Angles<N> angles;
     angles.init(p);
@@ -227,20 +254,16 @@ __global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int
         const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
         float4* mine = cs + buf * (tile * p.rot_dim / 4);
         const int rq = (ntok * nq + STEP - 1) / STEP, rounds = rq + (ntok * nk + STEP - 1) / STEP;
-        const T* const qi = static_cast<const T*>(p.in[0]) + tok0 * p.in_stride[0];
-        const T* const ki = static_cast<const T*>(p.in[1]) + tok0 * p.in_stride[1];
-        T* const qo = static_cast<T*>(p.out[0]) + tok0 * p.out_stride[0];
-        T* const ko = static_cast<T*>(p.out[1]) + tok0 * p.out_stride[1];
+        const char* const qi = static_cast<const char*>(p.in[0]) + tok0 * qis + x.first;
+        const char* const ki = static_cast<const char*>(p.in[1]) + tok0 * kis + x.first;
+        char* const qo = static_cast<char*>(p.out[0]) + tok0 * qos + x.first;
+        char* const ko = static_cast<char*>(p.out[1]) + tok0 * kos + x.first;
         int fi = 0;  // the round to load next, and its place
         Place at = q0, held[2];
-        uint4 r[2][2];
         auto fetch = [&](int b) {
             if (fi == rq) at = k0;
             const bool q = fi < rq, live = fi < rounds && at.t < ntok;
-            const T* v = q ? head_at(qi, at, static_cast<int>(p.in_stride[0]), p.headdim)
-                           : head_at(ki, at, static_cast<int>(p.in_stride[1]), p.headdim);
-            r[b][0] = load16(v, live ? s.v0 : -1);
-            r[b][1] = load16(v, live ? s.v1 : -1);
+            load_slot(q ? qi + head_at(at, qis, head) : ki + head_at(at, kis, head), live, x, r[b][0], r[b][1]);
             held[b] = at;
             at.next(q ? dtq : dtk, q ? dhq : dhk, q ? nq : nk);
             ++fi;
@@ -278,12 +301,8 @@ __global__ void __launch_bounds__(TPB, 3) norm_rope_kernel(NormRopeParams p, int
                 hi[2 * k + 1] = mul2(mul2(hi[2 * k + 1], inv), c);
             }
             if (s.rot) rotate<N, ADJ, false>(lo, hi, mine + (live ? w.t : 0) * (p.rot_dim / 4) + l, rs);
-            if (live) {
-                T* v = const_cast<T*>(i < rq ? head_at<T>(qo, w, static_cast<int>(p.out_stride[0]), p.headdim)
-                                             : head_at<T>(ko, w, static_cast<int>(p.out_stride[1]), p.headdim));
-                store16<T>(v, s.v0, lo);
-                store16<T>(v, s.v1, hi);
-            }
+            store_slot(i < rq ? qo + head_at(w, qos, head) : ko + head_at(w, kos, head), live, x, narrow2<T>(lo),
+                       narrow2<T>(hi));
         };
         // (a round is the whole CTA's: its shuffles take all lanes)
         for (int i = 0; i < rounds; i += 2) {
@@ -310,16 +329,20 @@ __global__ void __launch_bounds__(TPB, 2)
     const Slot s = slot_of<N>(l, p.headdim, p.rot_dim);
     const int rs = p.rot_dim / (2 * N);
     const float inv_d = 1.0f / static_cast<float>(p.headdim);
-    const T* const in = static_cast<const T*>(p.in[kd]);
-    const T* const dout = static_cast<const T*>(p.dout[kd]);
-    T* const din = static_cast<T*>(p.din[kd]);
+    const Reach x = reach_of<N>(s);
+    const char* const in = static_cast<const char*>(p.in[kd]) + x.first;
+    const char* const dout = static_cast<const char*>(p.dout[kd]) + x.first;
+    char* const din = static_cast<char*>(p.din[kd]) + x.first;
     // where the lane's first unit lies in a tile
     Place first;
     first.t = static_cast<int>(threadIdx.x) / LPU / heads;
     first.h = static_cast<int>(threadIdx.x) / LPU - first.t * heads;
     const int dt = STEP / heads, dh = STEP - dt * heads;
-    const int is = static_cast<int>(p.in_stride[kd]), es = static_cast<int>(p.dout_stride[kd]);
-    const int os = static_cast<int>(p.din_stride[kd]);
+    constexpr int E = sizeof(T);
+    const int head = p.headdim * E;  // bytes, as the strides
+    const int is = static_cast<int>(p.in_stride[kd]) * E, es = static_cast<int>(p.dout_stride[kd]) * E;
+    const int os = static_cast<int>(p.din_stride[kd]) * E;
+    uint4 r0 = make_uint4(0, 0, 0, 0), r1 = r0, q0 = r0, q1 = r0;
     fill_weights<N, LPU>(ws, p, kd, 1);
     float2 acc0[N / 2], acc1[N / 2];
 #pragma unroll
@@ -333,19 +356,14 @@ __global__ void __launch_bounds__(TPB, 2)
         const int ntok = static_cast<int>(tokens - tok0 < tile ? tokens - tok0 : tile);
         float4* mine = cs + buf * (tile * p.rot_dim / 4);
         const int rounds = (ntok * heads + STEP - 1) / STEP;
-        const T* const vi = in + tok0 * p.in_stride[kd];
-        const T* const ei = dout + tok0 * p.dout_stride[kd];
-        T* const vo = din + tok0 * p.din_stride[kd];
+        const char* const vi = in + tok0 * is;
+        const char* const ei = dout + tok0 * es;
+        char* const vo = din + tok0 * os;
         Place at = first, held;
-        uint4 r0, r1, q0, q1;
         auto fetch = [&]() {
             const bool live = at.t < ntok;
-            const T* v = head_at(vi, at, is, p.headdim);
-            const T* e = head_at(ei, at, es, p.headdim);
-            r0 = load16(v, live ? s.v0 : -1);
-            r1 = load16(v, live ? s.v1 : -1);
-            q0 = load16(e, live ? s.v0 : -1);
-            q1 = load16(e, live ? s.v1 : -1);
+            load_slot(vi + head_at(at, is, head), live, x, r0, r1);
+            load_slot(ei + head_at(at, es, head), live, x, q0, q1);
             held = at;
             at.next(dt, dh, heads);
         };
@@ -385,21 +403,18 @@ __global__ void __launch_bounds__(TPB, 2)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 m += __shfl_xor_sync(0xffffffffu, m, o);
             }
-            const float s1 = rsqrtf(fmaf(sum, inv_d, p.eps));
+            // (a lane without a unit holds an earlier one's values: it adds 0 to the sums)
+            const float s1 = live ? rsqrtf(fmaf(sum, inv_d, p.eps)) : 0.0f;
             const float2 inv = dup(s1), k = dup(-s1 * s1 * m * inv_d);
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {  // (a lane without a unit holds zeros)
+            for (int j = 0; j < N / 2; ++j) {
                 const float2 n0 = mul2(lo[j], inv), n1 = mul2(hi[j], inv);
                 acc0[j] = fma2(e0[j], n0, acc0[j]);
                 acc1[j] = fma2(e1[j], n1, acc1[j]);
                 e0[j] = fma2(n0, k, mul2(g0[j], inv));
                 e1[j] = fma2(n1, k, mul2(g1[j], inv));
             }
-            if (live) {
-                T* v = const_cast<T*>(head_at<T>(vo, w, os, p.headdim));
-                store16<T>(v, s.v0, e0);
-                store16<T>(v, s.v1, e1);
-            }
+            store_slot(vo + head_at(w, os, head), live, x, narrow2<T>(e0), narrow2<T>(e1));
         }
     }
     if (!p.dweight[kd]) return;
