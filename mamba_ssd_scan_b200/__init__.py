@@ -9,9 +9,10 @@ raises immediately.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
+import struct
 
 import torch
 
@@ -792,50 +793,95 @@ def ssd_gated_rmsnorm(y, z, weight, *, group: int | None = None, eps: float = 1e
 
 # ---------------------------------------------------------------------------
 # The gated linear recurrence, the head norm with the position rotation and the
-# convolution's gradient.
-def _need(t, name, shape, dtype, like):
-    """t must have this shape and dtype and lie, dense, on like's device."""
+# convolution's gradient.  Single-token steps and small batches are bound by the
+# host, so these calls check each tensor once, pack their arguments with struct
+# and read the stream's handle directly.
+_CODES = {_i64: "q", _i32: "i", ctypes.c_float: "f", _vp: "P", _sz: "N"}
+
+
+class _Entry:
+    """A library function that takes one argument struct and a stream."""
+
+    def __init__(self, lib, name, cls):
+        self.name = name
+        self.pack = struct.Struct("@" + "".join(_CODES[t] for _, t in cls._fields_) + "0q").pack
+        self.fn = lib[name]  # a handle of its own, with its own prototype
+        self.fn.restype = ctypes.c_int
+        self.fn.argtypes = [ctypes.c_char_p, _vp]
+
+
+def _entry(name, cls) -> _Entry:
+    lib = load_library()
+    try:
+        return lib.entries[name]
+    except (AttributeError, KeyError):
+        if not hasattr(lib, "entries"):
+            lib.entries = {}
+        return lib.entries.setdefault(name, _Entry(lib, name, cls))
+
+
+def _call(entry, stream, dev, *args):
+    """Calls the entry with the struct's fields in order; dev is the tensors' device."""
+    if dev < 0:
+        raise SsdError(SSD_ERR_INVALID_ARG, entry.name + " (host memory)")
+    if stream is not None:
+        handle = stream.cuda_stream
+    elif dev == torch.cuda.current_device():
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raise SsdError(SSD_ERR_INVALID_ARG, entry.name + " (tensors on another device than the current one)")
+    status = entry.fn(entry.pack(*args), handle)
+    if status != SSD_OK:
+        raise SsdError(status, entry.name)
+
+
+def _addr(t, name, shape, dtype, dev) -> int:
+    """The address of t, which must have this shape and dtype and lie, dense, on
+    device number dev (-1 = host)."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
-    return _ptr(t)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the other tensors")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _opt(t, name, shape, dtype, like):
-    return None if t is None else _need(t, name, shape, dtype, like)
-
-
-def _reset_ptr(reset, shape, like):
+def _reset_addr(reset, shape, dev) -> int:
     if reset is None:
-        return None
-    return _need(reset, "reset", shape, torch.bool if reset.dtype == torch.bool else torch.uint8, like)
+        return 0
+    return _addr(reset, "reset", shape, torch.bool if reset.dtype is torch.bool else torch.uint8, dev)
 
 
-def _allocating_on(stream):
+def _empty(shape, dtype, device, stream):
     """Outputs and scratch come from the pool of the stream that writes them, so
     that the allocator orders their reuse by that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _run(fn, a, stream, like):
-    """Calls the library function on the stream; like is one of the call's tensors."""
-    if not like.is_cuda:
-        raise SsdError(SSD_ERR_INVALID_ARG, fn.__name__ + " (host memory)")
-    _check(fn(ctypes.byref(a), _stream_ptr(stream)), fn.__name__)
-
-
-def _check_workspace(workspace, need, like):
-    if workspace.device != like.device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous and on {like.device}")
+def _workspace(workspace, need, like, dev, stream):
+    """(address, bytes) of the caller's workspace, or of a new one, and the tensor
+    that keeps it."""
+    if workspace is None:
+        workspace = _empty(need, torch.uint8, like.device, stream)
+        return workspace.data_ptr(), need, workspace
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous and on the device of the other tensors")
     have = workspace.numel() * workspace.element_size()
     if have < need:
         raise ValueError(f"workspace has {have} bytes, {need} are needed")
-    return workspace.data_ptr(), have
+    return workspace.data_ptr(), have, workspace
 
 
+_F32 = torch.float32
+
+
+@functools.lru_cache(maxsize=1024)
 def ssd_causal_conv1d_bwd_workspace_size(batch, seqlen, channels, width, dtype=torch.bfloat16) -> int:
     a = SsdConv1dBwdArgs(batch=batch, seqlen=seqlen, channels=channels, width=width,
                          dtype=SSD_BF16 if dtype == torch.bfloat16 else SSD_F32)
@@ -849,34 +895,30 @@ def ssd_causal_conv1d_bwd(x, weight, dy, bias=None, init_state=None, d_final=Non
     [b,C,K-1] float32 (the last three optional).  Returns a dict dx (x's dtype),
     dweight [C,K], dbias [C], d_init [b,C,K-1] (float32); ``out`` may hold
     preallocated tensors under the same keys."""
-    lib = load_library()
-    b, L, Cn = x.shape
+    entry = _entry("ssd_causal_conv1d_bwd", SsdConv1dBwdArgs)
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    b, L, Cn = shape
     K = weight.shape[1]
-    f32 = torch.float32
     state = (b, Cn, K - 1)
-    a = SsdConv1dBwdArgs(
-        batch=b, seqlen=L, channels=Cn, width=K, dtype=_dtype_code(x), activation=1 if activation else 0,
-        x=_ptr(x), weight=_need(weight, "weight", (Cn, K), f32, x), bias=_opt(bias, "bias", (Cn,), f32, x),
-        init_state=_opt(init_state, "init_state", state, f32, x) if K > 1 else None,
-        dy=_need(dy, "dy", x.shape, x.dtype, x),
-        d_final=_opt(d_final, "d_final", state, f32, x) if K > 1 else None)
-    need = int(lib.ssd_causal_conv1d_bwd_workspace_size(ctypes.byref(a)))
+    ins = (_addr(x, "x", shape, dt, dev), _addr(weight, "weight", (Cn, K), _F32, dev),
+           0 if bias is None else _addr(bias, "bias", (Cn,), _F32, dev),
+           0 if init_state is None or K == 1 else _addr(init_state, "init_state", state, _F32, dev),
+           _addr(dy, "dy", shape, dt, dev),
+           0 if d_final is None or K == 1 else _addr(d_final, "d_final", state, _F32, dev))
+    need = ssd_causal_conv1d_bwd_workspace_size(b, L, Cn, K, dt)
     if need == 0:
         raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_causal_conv1d_bwd (sizes)")
-    o = dict(out or {})
-    with _allocating_on(stream):
-        for name, shape, dtype in (("dx", x.shape, x.dtype), ("dweight", (Cn, K), f32),
-                                   ("dbias", (Cn,), f32), ("d_init", state, f32)):
-            if name not in o:
-                o[name] = torch.empty(shape, dtype=dtype, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    a.dx = _need(o["dx"], "dx", x.shape, x.dtype, x)
-    a.dweight = _need(o["dweight"], "dweight", (Cn, K), f32, x)
-    a.dbias = _need(o["dbias"], "dbias", (Cn,), f32, x)
-    a.d_init = _need(o["d_init"], "d_init", state, f32, x) if K > 1 else None
-    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, x)
-    _run(lib.ssd_causal_conv1d_bwd, a, stream, x)
+    o = dict(out) if out else {}
+    outs = []
+    for name, shp, dtype in (("dx", shape, dt), ("dweight", (Cn, K), _F32), ("dbias", (Cn,), _F32),
+                             ("d_init", state, _F32)):
+        if name not in o:
+            o[name] = _empty(shp, dtype, x.device, stream)
+        outs.append(_addr(o[name], name, shp, dtype, dev))
+    if K == 1:
+        outs[3] = 0
+    ws, size, keep = _workspace(workspace, need, x, dev, stream)
+    _call(entry, stream, dev, b, L, Cn, K, _dtype_code(x), 1 if activation else 0, *ins, *outs, ws, size)
     return o
 
 
@@ -890,28 +932,26 @@ def ssd_gated_scan(x, gate_a, gate_x, decay, init_state=None, reset=None, *, sca
     sequence.  Returns y, then the final state [b,C] and the states entering
     every 64th token [b,ceil(L/64),C] (for ssd_gated_scan_bwd), each when asked
     for or given."""
-    lib = load_library()
-    b, L, Cn = x.shape
-    f32 = torch.float32
-    kept = (b, (L + SSD_GATED_SCAN_INTERVAL - 1) // SSD_GATED_SCAN_INTERVAL, Cn)
-    with _allocating_on(stream):
-        if y is None:
-            y = torch.empty_like(x)
-        if final_state is None and return_final_state:
-            final_state = torch.empty((b, Cn), dtype=f32, device=x.device)
-        if states is None and return_states:
-            states = torch.empty(kept, dtype=f32, device=x.device)
-    a = SsdGatedScanArgs(
-        batch=b, seqlen=L, channels=Cn, dtype=_dtype_code(x), scale=scale, x=_ptr(x),
-        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
-        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x), decay=_need(decay, "decay", (Cn,), f32, x),
-        reset=_reset_ptr(reset, (b, L), x), init_state=_opt(init_state, "init_state", (b, Cn), f32, x),
-        y=_need(y, "y", x.shape, x.dtype, x),
-        final_state=_opt(final_state, "final_state", (b, Cn), f32, x),
-        states=_opt(states, "states", kept, f32, x))
-    _run(lib.ssd_gated_scan, a, stream, x)
-    res = (y,) + tuple(t for t in (final_state, states) if t is not None)
-    return res if len(res) > 1 else y
+    entry = _entry("ssd_gated_scan", SsdGatedScanArgs)
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    b, L, Cn = shape
+    state, kept = (b, Cn), (b, -(-L // SSD_GATED_SCAN_INTERVAL), Cn)
+    if y is None:
+        y = _empty(shape, dt, x.device, stream)
+    if final_state is None and return_final_state:
+        final_state = _empty(state, _F32, x.device, stream)
+    if states is None and return_states:
+        states = _empty(kept, _F32, x.device, stream)
+    _call(entry, stream, dev, b, L, Cn, _dtype_code(x), scale, _addr(x, "x", shape, dt, dev),
+          _addr(gate_a, "gate_a", shape, dt, dev), _addr(gate_x, "gate_x", shape, dt, dev),
+          _addr(decay, "decay", (Cn,), _F32, dev), _reset_addr(reset, (b, L), dev),
+          0 if init_state is None else _addr(init_state, "init_state", state, _F32, dev),
+          _addr(y, "y", shape, dt, dev),
+          0 if final_state is None else _addr(final_state, "final_state", state, _F32, dev),
+          0 if states is None else _addr(states, "states", kept, _F32, dev))
+    if final_state is None and states is None:
+        return y
+    return (y,) + tuple(t for t in (final_state, states) if t is not None)
 
 
 def ssd_gated_scan_check_status(stream=None) -> int:
@@ -921,6 +961,7 @@ def ssd_gated_scan_check_status(stream=None) -> int:
     return int(load_library().ssd_gated_scan_check_status(_stream_ptr(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
 def ssd_gated_scan_bwd_workspace_size(batch, seqlen, channels, dtype=torch.bfloat16) -> int:
     a = SsdGatedScanBwdArgs(batch=batch, seqlen=seqlen, channels=channels, scale=1.0,
                             dtype=SSD_BF16 if dtype == torch.bfloat16 else SSD_F32)
@@ -934,32 +975,27 @@ def ssd_gated_scan_bwd(x, gate_a, gate_x, decay, dy, states, reset=None, d_final
     inputs.  Returns a dict dx, dgate_a, dgate_x (x's dtype), ddecay [C] and
     d_init [b,C] (float32); ``out`` may hold preallocated tensors under the same
     keys."""
-    lib = load_library()
-    b, L, Cn = x.shape
-    f32 = torch.float32
-    kept = (b, (L + SSD_GATED_SCAN_INTERVAL - 1) // SSD_GATED_SCAN_INTERVAL, Cn)
-    a = SsdGatedScanBwdArgs(
-        batch=b, seqlen=L, channels=Cn, dtype=_dtype_code(x), scale=scale, x=_ptr(x),
-        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
-        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x), decay=_need(decay, "decay", (Cn,), f32, x),
-        reset=_reset_ptr(reset, (b, L), x), states=_need(states, "states", kept, f32, x),
-        dy=_need(dy, "dy", x.shape, x.dtype, x), d_final=_opt(d_final, "d_final", (b, Cn), f32, x))
-    need = int(lib.ssd_gated_scan_bwd_workspace_size(ctypes.byref(a)))
+    entry = _entry("ssd_gated_scan_bwd", SsdGatedScanBwdArgs)
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    b, L, Cn = shape
+    state, kept = (b, Cn), (b, -(-L // SSD_GATED_SCAN_INTERVAL), Cn)
+    ins = (_addr(x, "x", shape, dt, dev), _addr(gate_a, "gate_a", shape, dt, dev),
+           _addr(gate_x, "gate_x", shape, dt, dev), _addr(decay, "decay", (Cn,), _F32, dev),
+           _reset_addr(reset, (b, L), dev), _addr(states, "states", kept, _F32, dev),
+           _addr(dy, "dy", shape, dt, dev),
+           0 if d_final is None else _addr(d_final, "d_final", state, _F32, dev))
+    need = ssd_gated_scan_bwd_workspace_size(b, L, Cn, dt)
     if need == 0:
         raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_gated_scan_bwd (sizes)")
-    o = dict(out or {})
-    shapes = (("dx", x.shape, x.dtype), ("dgate_a", x.shape, x.dtype), ("dgate_x", x.shape, x.dtype),
-              ("ddecay", (Cn,), f32), ("d_init", (b, Cn), f32))
-    with _allocating_on(stream):
-        for name, shape, dtype in shapes:
-            if name not in o:
-                o[name] = torch.empty(shape, dtype=dtype, device=x.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    for name, shape, dtype in shapes:
-        setattr(a, name, _need(o[name], name, shape, dtype, x))
-    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, x)
-    _run(lib.ssd_gated_scan_bwd, a, stream, x)
+    o = dict(out) if out else {}
+    outs = []
+    for name, shp, dtype in (("dx", shape, dt), ("dgate_a", shape, dt), ("dgate_x", shape, dt),
+                             ("ddecay", (Cn,), _F32), ("d_init", state, _F32)):
+        if name not in o:
+            o[name] = _empty(shp, dtype, x.device, stream)
+        outs.append(_addr(o[name], name, shp, dtype, dev))
+    ws, size, keep = _workspace(workspace, need, x, dev, stream)
+    _call(entry, stream, dev, b, L, Cn, _dtype_code(x), scale, *ins, *outs, ws, size)
     return o
 
 
@@ -969,31 +1005,28 @@ def ssd_gated_state_update(state, x, gate_a, gate_x, decay, reset=None, *, scale
     one dtype, decay [C] and state [b,C] float32, reset [b] bool or uint8.  The
     state is updated in place unless ``new_state`` is given, which then receives
     it.  Returns y [b,C]."""
-    lib = load_library()
-    b, Cn = x.shape
+    entry = _entry("ssd_gated_state_update", SsdGatedStateUpdateArgs)
+    shape, dt, dev = x.shape, x.dtype, x.get_device()
+    b, Cn = shape
     if y is None:
-        with _allocating_on(stream):
-            y = torch.empty_like(x)
-    sp = _need(state, "state", (b, Cn), torch.float32, x)
-    a = SsdGatedStateUpdateArgs(
-        batch=b, channels=Cn, dtype=_dtype_code(x), scale=scale, state=sp, x=_ptr(x),
-        gate_a=_need(gate_a, "gate_a", x.shape, x.dtype, x),
-        gate_x=_need(gate_x, "gate_x", x.shape, x.dtype, x),
-        decay=_need(decay, "decay", (Cn,), torch.float32, x), reset=_reset_ptr(reset, (b,), x),
-        new_state=sp if new_state is None else _need(new_state, "new_state", (b, Cn), torch.float32, x),
-        y=_need(y, "y", x.shape, x.dtype, x))
-    _run(lib.ssd_gated_state_update, a, stream, x)
+        y = _empty(shape, dt, x.device, stream)
+    sp = _addr(state, "state", shape, _F32, dev)
+    _call(entry, stream, dev, b, Cn, _dtype_code(x), scale, sp, _addr(x, "x", shape, dt, dev),
+          _addr(gate_a, "gate_a", shape, dt, dev), _addr(gate_x, "gate_x", shape, dt, dev),
+          _addr(decay, "decay", (Cn,), _F32, dev), _reset_addr(reset, (b,), dev),
+          sp if new_state is None else _addr(new_state, "new_state", shape, _F32, dev),
+          _addr(y, "y", shape, dt, dev))
     return y
 
 
-def _head_rows(t, name, shape, like):
+def _head_rows(t, name, shape, dtype, dev):
     """(address, elements between tokens) of t [b,L,H,D], whose heads are dense
     within a token and whose tokens are evenly spaced (a slice of packed rows)."""
-    if t.dtype != like.dtype or t.device != like.device:
-        raise TypeError(f"{name} must be {like.dtype} on {like.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be {dtype} and on the device of the other tensors")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    b, L, H, D = t.shape
+    b, L, H, D = shape
     sb, sl, sh, sd = t.stride()
     if sd != 1 or (H > 1 and sh != D):
         raise ValueError(f"{name}: the heads of a token must be dense")
@@ -1002,20 +1035,19 @@ def _head_rows(t, name, shape, like):
     return t.data_ptr(), (sl if L > 1 else sb if b > 1 else H * D)
 
 
-def _qk_args(cls, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent):
-    b, L, hq, D = q.shape
-    f32 = torch.float32
-    a = cls(batch=b, seqlen=L, q_heads=hq, k_heads=0 if k is None else k.shape[2], headdim=D,
-            rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(), dtype=_dtype_code(q),
-            adjacent=1 if adjacent else 0, eps=eps, q_weight=_opt(q_weight, "q_weight", (D,), f32, q),
-            positions=_opt(positions, "positions", (b, L), torch.int64, q))
-    if inv_freq is not None:
-        a.inv_freq = _need(inv_freq, "inv_freq", (inv_freq.numel(),), f32, q)
-    a.q, a.q_stride = _head_rows(q, "q", None, q)
-    if k is not None:
-        a.k, a.k_stride = _head_rows(k, "k", (b, L, k.shape[2], D), q)
-        a.k_weight = _opt(k_weight, "k_weight", (D,), f32, q)
-    return a
+def _rotation(q, q_weight, k_weight, inv_freq, positions, dev):
+    """Addresses of the weights, frequencies and positions, and rot_dim."""
+    b, L, _, D = q.shape
+    n = 0 if inv_freq is None else inv_freq.numel()
+    return (0 if q_weight is None else _addr(q_weight, "q_weight", (D,), _F32, dev),
+            0 if k_weight is None else _addr(k_weight, "k_weight", (D,), _F32, dev),
+            0 if n == 0 else _addr(inv_freq, "inv_freq", (n,), _F32, dev),
+            0 if positions is None else _addr(positions, "positions", (b, L), torch.int64, dev)), 2 * n
+
+
+def _key_shape(q, k):
+    b, L, _, D = q.shape
+    return (b, L, k.shape[2], D)
 
 
 def ssd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, *, eps: float = 1e-5,
@@ -1029,20 +1061,28 @@ def ssd_qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions=None, *, eps:
     float32 or None (no rotation); positions [b,L] int64 or None (0, 1, ... in
     each row).  q_out / k_out may be q / k (in place) or such slices.  Returns
     (q_out, k_out)."""
-    lib = load_library()
-    a = _qk_args(SsdQkNormRopeArgs, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent)
-    with _allocating_on(stream):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    a.q_out, a.q_out_stride = _head_rows(q_out, "q_out", q.shape, q)
+    entry = _entry("ssd_qk_norm_rope", SsdQkNormRopeArgs)
+    qs, dt, dev = q.shape, q.dtype, q.get_device()
+    b, L, hq, D = qs
+    qp, q_stride = _head_rows(q, "q", qs, dt, dev)
+    if q_out is None:
+        q_out = _empty(qs, dt, q.device, stream)
+    qo, qo_stride = _head_rows(q_out, "q_out", qs, dt, dev)
+    hk = kp = ko = k_stride = ko_stride = 0
     if k is not None:
-        a.k_out, a.k_out_stride = _head_rows(k_out, "k_out", k.shape, q)
-    _run(lib.ssd_qk_norm_rope, a, stream, q)
+        ks = _key_shape(q, k)
+        hk = ks[2]
+        kp, k_stride = _head_rows(k, "k", ks, dt, dev)
+        if k_out is None:
+            k_out = _empty(ks, dt, q.device, stream)
+        ko, ko_stride = _head_rows(k_out, "k_out", ks, dt, dev)
+    ptrs, rot = _rotation(q, q_weight, k_weight, inv_freq, positions, dev)
+    _call(entry, stream, dev, b, L, hq, hk, D, rot, q_stride, k_stride, qo_stride, ko_stride, _dtype_code(q),
+          1 if adjacent else 0, eps, qp, kp, *ptrs, qo, ko)
     return q_out, (k_out if k is not None else None)
 
 
+@functools.lru_cache(maxsize=1024)
 def ssd_qk_norm_rope_bwd_workspace_size(batch, seqlen, q_heads, k_heads, headdim, rot_dim,
                                         dtype=torch.bfloat16) -> int:
     a = SsdQkNormRopeBwdArgs(batch=batch, seqlen=seqlen, q_heads=q_heads, k_heads=k_heads,
@@ -1059,30 +1099,31 @@ def ssd_qk_norm_rope_bwd(q, k, q_weight, k_weight, inv_freq, dq_out, dk_out, pos
     dk absent without k), dq_weight, dk_weight [D] (float32); ``out`` may hold
     preallocated tensors under the same keys, dq and dk also as slices of packed
     rows."""
-    lib = load_library()
-    a = _qk_args(SsdQkNormRopeBwdArgs, q, k, q_weight, k_weight, inv_freq, positions, eps, adjacent)
-    need = int(lib.ssd_qk_norm_rope_bwd_workspace_size(ctypes.byref(a)))
+    entry = _entry("ssd_qk_norm_rope_bwd", SsdQkNormRopeBwdArgs)
+    qs, dt, dev = q.shape, q.dtype, q.get_device()
+    b, L, hq, D = qs
+    o = dict(out) if out else {}
+
+    def side(name, t, d_out, shape):
+        """input, incoming gradient, outgoing gradient (address, stride), weight's gradient"""
+        if "d" + name not in o:
+            o["d" + name] = _empty(shape, dt, q.device, stream)
+        if f"d{name}_weight" not in o:
+            o[f"d{name}_weight"] = _empty(D, _F32, q.device, stream)
+        return (*_head_rows(t, name, shape, dt, dev), *_head_rows(d_out, f"d{name}_out", shape, dt, dev),
+                *_head_rows(o["d" + name], "d" + name, shape, dt, dev),
+                _addr(o[f"d{name}_weight"], f"d{name}_weight", (D,), _F32, dev))
+
+    ptrs, rot = _rotation(q, q_weight, k_weight, inv_freq, positions, dev)
+    hk = 0 if k is None else k.shape[2]
+    need = ssd_qk_norm_rope_bwd_workspace_size(b, L, hq, hk, D, rot, dt)
     if need == 0:
         raise SsdError(SSD_ERR_UNSUPPORTED, "ssd_qk_norm_rope_bwd (sizes)")
-    D = q.shape[3]
-    o = dict(out or {})
-    with _allocating_on(stream):
-        for name, t in (("q", q), ("k", k)):
-            if t is None:
-                continue
-            if "d" + name not in o:
-                o["d" + name] = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-            if f"d{name}_weight" not in o:
-                o[f"d{name}_weight"] = torch.empty(D, dtype=torch.float32, device=t.device)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    a.dq_out, a.dq_out_stride = _head_rows(dq_out, "dq_out", q.shape, q)
-    a.dq, a.dq_stride = _head_rows(o["dq"], "dq", q.shape, q)
-    a.dq_weight = _need(o["dq_weight"], "dq_weight", (D,), torch.float32, q)
+    qp, q_stride, qg, qg_stride, dq, dq_stride, dqw = side("q", q, dq_out, qs)
+    kp = k_stride = kg = kg_stride = dk = dk_stride = dkw = 0
     if k is not None:
-        a.dk_out, a.dk_out_stride = _head_rows(dk_out, "dk_out", k.shape, q)
-        a.dk, a.dk_stride = _head_rows(o["dk"], "dk", k.shape, q)
-        a.dk_weight = _need(o["dk_weight"], "dk_weight", (D,), torch.float32, q)
-    a.workspace, a.workspace_bytes = _check_workspace(workspace, need, q)
-    _run(lib.ssd_qk_norm_rope_bwd, a, stream, q)
+        kp, k_stride, kg, kg_stride, dk, dk_stride, dkw = side("k", k, dk_out, _key_shape(q, k))
+    ws, size, keep = _workspace(workspace, need, q, dev, stream)
+    _call(entry, stream, dev, b, L, hq, hk, D, rot, q_stride, k_stride, qg_stride, kg_stride, dq_stride, dk_stride,
+          _dtype_code(q), 1 if adjacent else 0, eps, qp, kp, *ptrs, qg, kg, dq, dk, dqw, dkw, ws, size)
     return o
