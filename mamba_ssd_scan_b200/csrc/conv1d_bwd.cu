@@ -250,11 +250,10 @@ ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels) {
 
 template <typename T, int K, bool ACT>
 cudaError_t launch_act(const ConvBwdParams& p, const ConvBwdMaps& m, const ConvGrid& g, cudaStream_t s) {
-    const auto kern = conv1d_bwd_kernel<T, K, ACT>;
-    const int smem = NW * kWarpBytes<T>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = NW * kWarpBytes<T>;
+    const cudaError_t e = prepare_kernel<conv1d_bwd_kernel<T, K, ACT>>(smem, false);
     if (e != cudaSuccess) return e;
-    kern<<<static_cast<unsigned>((g.warps + NW - 1) / NW), NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg),
+    conv1d_bwd_kernel<T, K, ACT><<<static_cast<unsigned>((g.warps + NW - 1) / NW), NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg),
                                                                              g.warps);
     return cudaGetLastError();
 }

@@ -803,22 +803,18 @@ int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern ke
     return best;
 }
 
-// T, BWD: one table of held clusters per kernel family.
-template <typename T, bool BWD, typename Kern, typename... Args>
-cudaError_t launch_clusters(Kern kern, const GatedScanParams& p, size_t smem, cudaStream_t s,
-                            int* cluster, const Args&... args) {
+template <auto Kern, typename... Args>
+cudaError_t launch_clusters(const GatedScanParams& p, int tile, size_t smem, cudaStream_t s, int* cluster,
+                            const Args&... args) {
     static std::atomic<int> held[kMaxDevices][kMaxCluster + 1];
-    // (attributes are the device's own: set on every call)
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const cudaError_t e = prepare_kernel<Kern>(static_cast<int>(smem), true);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (p.channels + CPB - 1) / CPB;
-    constexpr int tile = NW * (BWD ? TPT : kFwdTokens<T>);
-    const int cl = cluster_size(held, kern, smem, blocks, p.batch, (p.seqlen + tile - 1) / tile);
+    const int cl = cluster_size(held, Kern, smem, blocks, p.batch, (p.seqlen + tile - 1) / tile);
     *cluster = cl;
     cudaLaunchAttribute attr;
     const cudaLaunchConfig_t cfg = cluster_config(&attr, blocks, p.batch, cl, smem, s);
-    return cudaLaunchKernelEx(&cfg, kern, p, args..., cl, static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP)));
+    return cudaLaunchKernelEx(&cfg, Kern, p, args..., cl, static_cast<int>(debug_withhold(SSD_DEBUG_GATED_MAP)));
 }
 
 }  // namespace
@@ -837,8 +833,8 @@ template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cu
         if (!make_tmap_rows(a.first, a.second, sizeof(T) == 2, p.channels, p.seqlen, p.batch, tile))
             return cudaErrorInvalidValue;
     int cl = 1;
-    return p.reset ? launch_clusters<T, false>(gated_scan_kernel<T, true>, p, smem, s, &cl, m)
-                   : launch_clusters<T, false>(gated_scan_kernel<T, false>, p, smem, s, &cl, m);
+    return p.reset ? launch_clusters<gated_scan_kernel<T, true>>(p, tile, smem, s, &cl, m)
+                   : launch_clusters<gated_scan_kernel<T, false>>(p, tile, smem, s, &cl, m);
 }
 
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s) {
@@ -852,8 +848,8 @@ template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p
             return cudaErrorInvalidValue;
     int cl = 1;
     const cudaError_t e =
-        p.reset ? launch_clusters<T, true>(gated_scan_bwd_kernel<T, true>, p, smem, s, &cl, m)
-                : launch_clusters<T, true>(gated_scan_bwd_kernel<T, false>, p, smem, s, &cl, m);
+        p.reset ? launch_clusters<gated_scan_bwd_kernel<T, true>>(p, TILE, smem, s, &cl, m)
+                : launch_clusters<gated_scan_bwd_kernel<T, false>>(p, TILE, smem, s, &cl, m);
     if (e != cudaSuccess) return e;
     return launch_kernel(gated_scan_finish_kernel, dim3(static_cast<unsigned>((p.channels + 31) / 32)),
                          dim3(kColSumThreads), 0, s, true, p, p.batch * cl);

@@ -2,9 +2,26 @@
 // rotation and the convolution's gradient as api.cu sees them.
 #pragma once
 
+#include <atomic>
+
 #include "internal.cuh"
 
 namespace ssd {
+
+// A kernel's attributes on the current device, set at its first launch there:
+// dynamic shared memory up to `smem` bytes, and clusters beyond 8 CTAs.
+template <auto Kern> cudaError_t prepare_kernel(int smem, bool clusters) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && clusters) e = cudaFuncSetAttribute(Kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // One call of the gated linear recurrence: forward (y, final_state, states
 // out) or backward (states in, dy ... out).

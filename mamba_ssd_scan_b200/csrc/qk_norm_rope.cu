@@ -493,17 +493,15 @@ int64_t norm_rope_bwd_rows() { return kBwdCtas; }
 
 namespace {
 
-// (dynamic shared memory beyond 48 KB is asked for: two tiles' angles can take 64 KB)
-template <typename Kern> cudaError_t allow_smem(Kern kern) {
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-}
+constexpr int kMaxSmem = 65536;  // two tiles' angles
 
 template <typename T, int LPU> cudaError_t launch_fwd(const NormRopeParams& p, cudaStream_t s) {
     const int64_t tokens = p.batch * p.seqlen, slots = 3 * device_sms();
     const int tile = tile_tokens(tokens, p.heads[0] + p.heads[1], LPU, p.rot_dim, slots);
     const int64_t ntiles = (tokens + tile - 1) / tile, grid = ntiles < slots ? ntiles : slots;
     const auto kern = p.adjacent ? norm_rope_kernel<T, true, LPU> : norm_rope_kernel<T, false, LPU>;
-    const cudaError_t e = allow_smem(kern);
+    const cudaError_t e = p.adjacent ? prepare_kernel<norm_rope_kernel<T, true, LPU>>(kMaxSmem, false)
+                                     : prepare_kernel<norm_rope_kernel<T, false, LPU>>(kMaxSmem, false);
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(grid), TPB, 2 * static_cast<size_t>(tile) * p.rot_dim * 4, s>>>(p, tile, tokens);
     return cudaGetLastError();
@@ -523,7 +521,8 @@ template <typename T, int LPU> cudaError_t launch_bwd(const NormRopeParams& p, c
     if (p.heads[1] == 0) ck = 0;
     const size_t smem = 2 * static_cast<size_t>(tile) * p.rot_dim * 4;
     const auto kern = p.adjacent ? norm_rope_bwd_kernel<T, true, LPU> : norm_rope_bwd_kernel<T, false, LPU>;
-    cudaError_t e = allow_smem(kern);
+    cudaError_t e = p.adjacent ? prepare_kernel<norm_rope_bwd_kernel<T, true, LPU>>(kMaxSmem, false)
+                               : prepare_kernel<norm_rope_bwd_kernel<T, false, LPU>>(kMaxSmem, false);
     if (e != cudaSuccess) return e;
     kern<<<static_cast<unsigned>(cq + ck), TPB, smem, s>>>(p, tile, tokens, static_cast<int>(cq));
     e = cudaGetLastError();
