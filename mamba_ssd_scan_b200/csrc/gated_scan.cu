@@ -101,9 +101,9 @@ __device__ __forceinline__ float2 read_gates(uint32_t raw, uint32_t least) {
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(raw) : "r"(least));
     return Pair<__nv_bfloat16>::widen(raw);
 }
-// one widened gate, cut off alike
-template <bool EXACT> __device__ __forceinline__ float2 one_gate(float v, float least) {
-    return dup(EXACT ? v : max_nan(v, least));
+// widened gates, cut off alike
+template <bool EXACT> __device__ __forceinline__ float2 least_gates(float2 v, float least) {
+    return EXACT ? v : make_float2(max_nan(v.x, least), max_nan(v.y, least));
 }
 constexpr uint32_t kLeastA = 0xC2AEC2AEu;  // -87: e^87 < 2^126
 constexpr uint32_t kLeastX = 0xC226C226u;  // -41.5: e^41.5 < 2^60
@@ -713,25 +713,78 @@ __global__ void __launch_bounds__(kColSumThreads) gated_scan_finish_kernel(Gated
     });
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) gated_update_kernel(GatedUpdateParams p) {
+// The decode step: a thread takes 4 channels of R batch rows, so that the
+// channels' softplus is formed once for all of them and R rows' loads are in
+// flight together.  Bandwidth-bound (the state in and out, four inputs and
+// outputs); for a single row the launch is all there is, and consecutive steps
+// overlap theirs by programmatic dependent launch.
+constexpr int kUpdateThreads = 128;
+template <typename T> struct Quad4;
+template <> struct Quad4<float> {
+    using Raw = float4;
+    static __device__ __forceinline__ void widen(Raw r, float2& a, float2& b) {
+        a = make_float2(r.x, r.y);
+        b = make_float2(r.z, r.w);
+    }
+    static __device__ __forceinline__ Raw narrow(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
+};
+template <> struct Quad4<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void widen(Raw r, float2& a, float2& b) {
+        a = Pair<__nv_bfloat16>::widen(r.x);
+        b = Pair<__nv_bfloat16>::widen(r.y);
+    }
+    static __device__ __forceinline__ Raw narrow(float2 a, float2 b) {
+        return make_uint2(Pair<__nv_bfloat16>::narrow(a), Pair<__nv_bfloat16>::narrow(b));
+    }
+};
+
+template <typename T, int R>
+__global__ void __launch_bounds__(kUpdateThreads) gated_update_kernel(GatedUpdateParams p) {
     constexpr bool EXACT = sizeof(T) == 4;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    if (i >= p.batch * p.channels) return;
-    const int64_t c = i % p.channels;
+    using Q = Quad4<T>;
+    using Raw = typename Q::Raw;
+    const int64_t quads = p.channels / 4, quad = static_cast<int64_t>(blockIdx.x) * kUpdateThreads + threadIdx.x;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.y) * R;
     grid_dep_wait();
     grid_dep_launch();
-    const bool rs = p.reset && p.reset[i / p.channels];
-    float2 r, ii, em1, a;
-    sigmas<EXACT>(one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_a)[i]), -87.0f),
-                  one_gate<EXACT>(to_f32(static_cast<const T*>(p.gate_x)[i]), -41.5f), r, ii);
-    decays<EXACT, false>(mul2(dup(-p.scale * softplus_f32(p.decay[c])), r), em1, a);
-    if (rs) em1 = dup(-1.0f);
-    const float h = p.state[i];
-    const float hn = (rs ? 0.0f : fmaf(em1.x, h, h)) +
-                     input_weight(em1).x * (ii.x * to_f32(static_cast<const T*>(p.x)[i]));
-    p.new_state[i] = hn;
-    static_cast<T*>(p.y)[i] = from_f32<T>(hn);
+    if (quad >= quads) return;
+    float4 st[R];
+    Raw x[R], ga[R], gx[R];
+    bool rs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int64_t row = row0 + r < p.batch ? row0 + r : p.batch - 1, i = row * quads + quad;
+        st[r] = reinterpret_cast<const float4*>(p.state)[i];
+        x[r] = static_cast<const Raw*>(p.x)[i];
+        ga[r] = static_cast<const Raw*>(p.gate_a)[i];
+        gx[r] = static_cast<const Raw*>(p.gate_x)[i];
+        rs[r] = p.reset && p.reset[row];
+    }
+    const float4 d = reinterpret_cast<const float4*>(p.decay)[quad];
+    const float2 k[2] = {make_float2(-p.scale * softplus_f32(d.x), -p.scale * softplus_f32(d.y)),
+                         make_float2(-p.scale * softplus_f32(d.z), -p.scale * softplus_f32(d.w))};
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (row0 + r >= p.batch) break;
+        float2 xv[2], av[2], iv[2];
+        Q::widen(x[r], xv[0], xv[1]);
+        Q::widen(ga[r], av[0], av[1]);
+        Q::widen(gx[r], iv[0], iv[1]);
+        float2 h[2] = {make_float2(st[r].x, st[r].y), make_float2(st[r].z, st[r].w)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float2 rg, ig, em1, a;
+            sigmas<EXACT>(least_gates<EXACT>(av[j], -87.0f), least_gates<EXACT>(iv[j], -41.5f), rg, ig);
+            decays<EXACT, false>(mul2(k[j], rg), em1, a);
+            if (rs[r]) em1 = dup(-1.0f);
+            const float2 u = mul2(mul2(input_weight(em1), ig), xv[j]);
+            h[j] = rs[r] ? u : add2(h[j], fma2(em1, h[j], u));
+        }
+        const int64_t i = (row0 + r) * quads + quad;
+        reinterpret_cast<float4*>(p.new_state)[i] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        static_cast<Raw*>(p.y)[i] = Q::narrow(h[0], h[1]);
+    }
 }
 
 int device_sms() {
@@ -855,10 +908,15 @@ template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p
                          dim3(kColSumThreads), 0, s, true, p, p.batch * cl);
 }
 
+template <typename T, int R> cudaError_t launch_update_rows(const GatedUpdateParams& p, cudaStream_t s) {
+    const dim3 grid(static_cast<unsigned>((p.channels / 4 + kUpdateThreads - 1) / kUpdateThreads),
+                    static_cast<unsigned>((p.batch + R - 1) / R));
+    return launch_kernel(gated_update_kernel<T, R>, grid, dim3(kUpdateThreads), 0, s, true, p);
+}
 template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p, cudaStream_t s) {
-    const int64_t n = p.batch * p.channels;
-    return launch_kernel(gated_update_kernel<T>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
-                         0, s, true, p);
+    // four rows per thread where that still gives every SM four CTAs
+    const int64_t ctas = (p.channels / 4 + kUpdateThreads - 1) / kUpdateThreads * ((p.batch + 3) / 4);
+    return ctas >= 4 * device_sms() ? launch_update_rows<T, 4>(p, s) : launch_update_rows<T, 1>(p, s);
 }
 
 cudaError_t gated_scan_take_status(int* v, cudaStream_t s) {
