@@ -815,9 +815,11 @@ cudaLaunchConfig_t cluster_config(cudaLaunchAttribute* attr, int64_t blocks, int
 // CTAs per cluster.  More of them cut the rounds a sequence takes, but share the
 // SMs, add an exchange per round and, beyond what the device holds at once
 // (asked of the runtime, once per device), run in waves.  A round measured
-// about 1.3 + 0.5 k us with k CTAs on an SM, and 0.7 us more in a cluster; the
-// size with the least waves x rounds x that is taken.  (b1 L65536 C1536: 15,
-// 256 us; 10, 281 us; 8, 345 us.  b8 L4096 C2048: 1, 145 us; 2, 158 us.)
+// about 1.3 + 0.5 k us with k CTAs on an SM, 0.7 us more in a cluster, and the
+// start of a wave about one and a half rounds; the size with the least sum is
+// taken.  (bf16 b1 L65536 C1536: 15, 232 us; 10, 255; 8, 302.  bf16 gradient
+// b8 L4096 C2048: 1, 226 us; 2, 247; b1 L65536 C1536: 10, 425; 8, 488.  fp32
+// gradient b2 L777 C1536: 5, 36 us; 13, 42; 1, 73.)
 constexpr int kMaxDevices = 64;
 template <typename Kern>
 int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern kern, size_t smem,
@@ -846,7 +848,7 @@ int cluster_size(std::atomic<int> (&held)[kMaxDevices][kMaxCluster + 1], Kern ke
         if (n < 1) continue;
         const int64_t waves = (clusters + n - 1) / n, rounds = (tiles + cl - 1) / cl;
         const double share = static_cast<double>(clusters < n ? clusters : n) * cl / sms;
-        const double cost = static_cast<double>(waves * rounds) *
+        const double cost = static_cast<double>(waves) * (static_cast<double>(rounds) + 1.5) *
                             (1.3 + 0.5 * (share < 1.0 ? 1.0 : share) + (cl > 1 ? 0.7 : 0.0));
         if (least == 0.0 || cost < least) {
             least = cost;
