@@ -824,12 +824,14 @@ def _call(entry, stream, dev, *args):
     """Calls the entry with the struct's fields in order; dev is the tensors' device."""
     if dev < 0:
         raise SsdError(SSD_ERR_INVALID_ARG, entry.name + " (host memory)")
-    if stream is not None:
-        handle = stream.cuda_stream
-    elif dev == torch.cuda.current_device():
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    else:
+    if dev != torch.cuda.current_device():
         raise SsdError(SSD_ERR_INVALID_ARG, entry.name + " (tensors on another device than the current one)")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index == dev:
+        handle = stream.cuda_stream
+    else:
+        raise SsdError(SSD_ERR_INVALID_ARG, entry.name + " (stream of another device than the tensors)")
     status = entry.fn(entry.pack(*args), handle)
     if status != SSD_OK:
         raise SsdError(status, entry.name)

@@ -183,3 +183,23 @@ def test_binding_checks_shapes_and_types(lib):
                     (dict(weight=torch.zeros(16, 9)), m.SsdError), ({}, m.SsdError)):
         with pytest.raises(exc):
             m.ssd_causal_conv1d_bwd(**{**dict(x=x, weight=xw, dy=x), **kw})
+
+
+def test_streams_and_devices_that_do_not_match_are_refused(monkeypatch):
+    """Nothing is launched unless the tensors, the stream and the current device
+    are the same one."""
+    import types
+    import mamba_ssd_scan_b200 as m
+    calls = []
+    entry = types.SimpleNamespace(name="entry", pack=lambda *a: b"",
+                                  fn=lambda args, handle: calls.append(handle) or 0)
+
+    def stream(index):
+        return types.SimpleNamespace(cuda_stream=1000 + index, device_index=index)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for s, dev in ((None, 1), (stream(1), 1), (stream(0), 1), (stream(1), 0), (None, -1), (stream(0), -1)):
+        with pytest.raises(m.SsdError):
+            m._call(entry, s, dev)
+    assert not calls
+    m._call(entry, stream(0), 0)
+    assert calls == [1000]
