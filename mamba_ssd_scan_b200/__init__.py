@@ -857,18 +857,25 @@ def _reset_addr(reset, shape, dev) -> int:
     return _addr(reset, "reset", shape, torch.bool if reset.dtype is torch.bool else torch.uint8, dev)
 
 
-def _empty(shape, dtype, like, stream):
-    """A dense tensor on like's device, from the pool of the stream that will write
-    it, so that the allocator orders its reuse by that stream.  (empty_strided
-    takes half the time of empty.)"""
-    if stream is not None:
-        with torch.cuda.stream(stream):
-            return _empty(shape, dtype, like, None)
+@functools.lru_cache(maxsize=1024)
+def _dense(shape):
     strides, n = [], 1
     for d in reversed(shape):
         strides.append(n)
         n *= d if d > 0 else 1
-    return torch.empty_strided(shape, strides[::-1], dtype=dtype, device=like.device)
+    return tuple(strides[::-1])
+
+
+def _empty(shape, dtype, like, stream):
+    """A dense tensor on like's device, from the pool of the stream that will write
+    it, so that the allocator orders its reuse by that stream.  (empty_like takes
+    half the time of empty, empty_strided two thirds.)"""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, like, None)
+    if like.dtype is dtype and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty_strided(shape, _dense(shape), dtype=dtype, device=like.device)
 
 
 def _output(given, name, shape, dtype, like, dev, stream):
