@@ -506,7 +506,8 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
  *   log a_t = -scale softplus(decay_c) r_t
  *   h_t = a_t h_{t-1} + sqrt(1 - a_t^2) i_t x_t;   y_t = h_t
  * Where reset is nonzero a token starts a new sequence: a_t = 0, so h_t =
- * i_t x_t (packed documents; at token 0 it drops init_state).
+ * i_t x_t (packed documents; at token 0 it drops init_state), whatever its
+ * gate_a holds.
  * Layouts: x, gate_a, gate_x, y [batch, seqlen, channels] dtype; decay
  *   [channels] fp32; reset [batch, seqlen] bytes or NULL (= none);
  *   init_state, final_state [batch, channels] fp32 or NULL (= 0 / not
@@ -514,7 +515,9 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
  *   channels] fp32 or NULL: receives the state before tokens 0, 64, 128, ...
  *   (states[:, 0] = init_state), which ssd_gated_scan_bwd takes.
  * Gates, decays and the carried state are fp32 for both types; y is the fp32
- * state rounded once.  Results do not depend on timing (no atomics).
+ * state rounded once.  A gate_a below about -46 next to a strongly negative
+ * gate_x (below -87 in any case) counts as shut: r = i = 0.  Results do not
+ * depend on timing (no atomics).
  * Supported: channels a multiple of 8 (bf16) or 4 (fp32), batch <= 65535,
  *   seqlen < 2^31 (else SSD_ERR_UNSUPPORTED); scale > 0 and finite; every
  *   pointer but reset 16-byte aligned (else SSD_ERR_INVALID_ARG).  Outputs
@@ -611,8 +614,9 @@ ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* args, void*
  *   out_a = u_a cos f - u_b sin f,  out_b = u_a sin f + u_b cos f,
  *   f = position * inv_freq[j],  j < rot_dim / 2
  * for the pairs (a, b) = (j, j + rot_dim / 2), or (2j, 2j + 1) with `adjacent`;
- * elements from rot_dim on are not rotated.  The angle is formed in fp64 and
- * reduced by whole turns before its cosine and sine (fp32).
+ * elements from rot_dim on are not rotated.  The turns per position, inv_freq /
+ * (2 pi), are formed in fp64 and held as a 64-bit fraction, so that whole turns
+ * drop out of the product with the position exactly; cosine and sine are fp32.
  * Layouts: q, q_out: batch * seqlen tokens q_stride / q_out_stride elements
  *   apart, each with q_heads dense heads of headdim elements, dtype; k, k_out
  *   alike (NULL with k_heads = 0).  So slices of one packed row per token are

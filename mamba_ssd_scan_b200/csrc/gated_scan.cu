@@ -3,21 +3,34 @@
 //
 // A step h <- a h + u is an affine map, and maps compose: (A, H) after (A', H')
 // is (A A', A H' + H).  So a sequence is cut into groups of 8 consecutive
-// tokens, each thread runs its group from zero, the groups' maps are composed,
-// and each thread then replays its group from the state that enters it.  The
-// replay costs two packed operations per token on values that are still in
-// registers, while the gates (about 4 special-function results per element)
-// are formed once and the inputs are read once.
+// tokens (4 in the fp32 forward), each thread runs its group from zero, the
+// groups' maps are composed, and each thread then replays its group from the
+// state that enters it.  The replay costs two packed operations per token on
+// values that are still in registers, while the gates (about 4
+// special-function results per element) are formed once and the inputs are
+// read once.
 //
 // A compute warp takes one group of tokens of 64 channels (a pair per lane);
-// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens),
-// and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
+// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens;
+// 32 in the fp32 forward), and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
 // tile's map, sends it to the cluster's CTAs through distributed shared memory
 // (asynchronous stores that complete on the receiver's mbarrier), and hands
 // each group its entering state.  The order of composition is fixed, so
 // results do not depend on timing; there is no workspace and no wait on another
 // cluster.  Every mbarrier wait is bounded: on expiry the CTA raises its abort
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
+//
+// Measured (B200, L2 flushed; share of the measured copy bandwidth over the
+// call's least bytes).  Forward, bf16: b6 L4096 C4736 176 us (82 %), b8 L4096
+// C2048 129 us (65 %), b1 L65536 C1536 229 us (55 %); fp32: b8 L4096 C2048 200
+// us (83 %).  Gradient, bf16: b4 L4096 C4736 228 us (74 %), b8 L4096 C2048 226
+// us (65 %), b1 L65536 C1536 425 us (52 %).  Where the CTAs fill the SMs evenly
+// the forward is bound by its instructions (57 per channel pair and token; issue
+// slots 55 % busy, the special-function pipe 62 %) as much as by its bytes, and
+// the gradient by its own (issue 54 %, FMA pipe 46 %, at two CTAs per SM).  b8 C2048
+// is 256 CTAs on 148 SMs, a third of which take one where the others take two;
+// halves of the sequence in clusters of two cost more than they even out.
+// Long sequences of few channels wait for the exchange, once per round.
 #include <atomic>
 #include <type_traits>
 #include <utility>
@@ -400,8 +413,9 @@ __global__ void __launch_bounds__(kThreads, 3)
             auto form = [&](auto is_slow) {
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
-                    float2 r, i, a;
-                    sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r, i);
+                    float2 r, i, a, ga = read_gates(*at(2, j), kLeastA);
+                    if (RESET && ((rst >> j) & 1)) ga = dup(0.0f);  // not used: whatever it holds
+                    sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r, i);
                     decays<EXACT, decltype(is_slow)::value>(mul2(k, r), em1[j], a);
                     float2 n = input_weight(em1[j]);
                     if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
@@ -610,11 +624,12 @@ __global__ void __launch_bounds__(kThreads, 2)
             auto form = [&](auto is_slow) {
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
-                    float2 a;
-                    sigmas<EXACT>(read_gates(*at(2, j), kLeastA), read_gates(*at(1, j), kLeastX), r[j], i[j]);
+                    const bool rs = RESET && ((rst >> j) & 1);
+                    float2 a, ga = read_gates(*at(2, j), kLeastA);
+                    if (rs) ga = dup(0.0f);
+                    sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r[j], i[j]);
                     decays<EXACT, decltype(is_slow)::value>(mul2(k, r[j]), em1[j], a);
                     float2 n = input_weight(em1[j]);
-                    const bool rs = RESET && ((rst >> j) & 1);
                     if (rs) n = dup(1.0f);
                     float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
                     if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
@@ -715,9 +730,11 @@ __global__ void __launch_bounds__(kColSumThreads) gated_scan_finish_kernel(Gated
 
 // The decode step: a thread takes 4 channels of R batch rows, so that the
 // channels' softplus is formed once for all of them and R rows' loads are in
-// flight together.  Bandwidth-bound (the state in and out, four inputs and
-// outputs); for a single row the launch is all there is, and consecutive steps
-// overlap theirs by programmatic dependent launch.
+// flight together.  Bandwidth-bound at large batches (the state in and out, four
+// inputs and outputs; fp32 b512 C5120 18.4 us between events, 52 MB that mostly
+// stay in L2); a small one is its launch, and consecutive steps overlap theirs
+// by programmatic dependent launch (bf16 b256 C5120 8 us a step, one row of
+// 1536 channels the same).
 constexpr int kUpdateThreads = 128;
 template <typename T> struct Quad4;
 template <> struct Quad4<float> {
@@ -775,6 +792,7 @@ __global__ void __launch_bounds__(kUpdateThreads) gated_update_kernel(GatedUpdat
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float2 rg, ig, em1, a;
+            if (rs[r]) av[j] = dup(0.0f);
             sigmas<EXACT>(least_gates<EXACT>(av[j], -87.0f), least_gates<EXACT>(iv[j], -41.5f), rg, ig);
             decays<EXACT, false>(mul2(k[j], rg), em1, a);
             if (rs[r]) em1 = dup(-1.0f);

@@ -134,6 +134,35 @@ def test_gated_scan_restart_drops_infinities():
     assert torch.equal(gd["ddecay"][ok], gc["ddecay"][ok])
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("gate", [-60.0, -100.0, -3e38, float("-inf"), float("inf"), float("nan")])
+def test_gated_scan_restart_does_not_use_its_decay_gate(dtype, gate):
+    """A restarting token is i x whatever its gate_a (a padded or masked place may
+    hold anything there): bitwise what a gate of 0 gives, in the scan, its gradient
+    and the decode step; and that against the definition."""
+    b, L, C = 2, 200, 24
+    d, dy, df = scan_inputs(b, L, C, dtype, seed=11, init=True)
+    d["reset"] = torch.zeros((b, L), dtype=torch.uint8)
+    d["reset"][:, [0, 63, 64, 130, 199]] = 1
+    runs = []
+    for v in (0.0, gate):
+        d["gate_a"][d["reset"] != 0] = v
+        g = dev(d)
+        y, fin, st = ssd.ssd_gated_scan(**g, return_final_state=True, return_states=True)
+        h0 = g.pop("init_state")
+        o = ssd.ssd_gated_scan_bwd(dy=dy.to(DEV), states=st, d_final=df.to(DEV), **g)
+        new = torch.empty_like(h0)
+        step = ssd.ssd_gated_state_update(h0, *(g[k][:, 64].contiguous() for k in ("x", "gate_a", "gate_x")),
+                                          g["decay"], g["reset"][:, 64].contiguous(), new_state=new)
+        runs.append({"y": y, "final": fin, "states": st, "step": step, "new": new, **o})
+        if v == 0.0:
+            ref = om.gated_scan(d["x"], d["gate_a"], d["gate_x"], d["decay"], d["init_state"], d["reset"])
+            within(y, ref["y"], ref["e_y"], "y")
+    for k in runs[0]:
+        assert torch.equal(runs[0][k], runs[1][k]), k
+    assert (runs[1]["dgate_a"][:, [0, 63, 64, 130, 199]] == 0).all()
+
+
 def test_gated_scan_split_decode_and_bool_reset():
     """Resuming from the final state and stepping token by token give the scan's
     states, each within both bounds."""
