@@ -237,6 +237,17 @@ __device__ __forceinline__ float2 apply(float4 m, bool restart, float2 h) {
     return restart ? H : fma2(make_float2(m.x, m.y), h, H);
 }
 
+// f(slow, restarts) for the two properties of a group that change its code
+template <bool RESET, typename F> __device__ __forceinline__ void by_group(bool slow, uint32_t rst, F f) {
+    if (RESET && rst != 0) {
+        if (slow) f(std::true_type(), std::true_type());
+        else f(std::false_type(), std::true_type());
+    } else {
+        if (slow) f(std::true_type(), std::false_type());
+        else f(std::false_type(), std::false_type());
+    }
+}
+
 struct Exchange {
     float4 group_map[NW][32];             // this CTA's groups
     float4 tile_map[2][kMaxCluster][32];  // the cluster's tiles, two rounds
@@ -410,32 +421,31 @@ __global__ void __launch_bounds__(kThreads, 3)
             wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
             // the gates and the group's map
             float2 em1[TPT], u[TPT];
-            auto form = [&](auto is_slow) {
+            float2 A = dup(1.0f), H = dup(0.0f);
+            by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
+                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
                     float2 r, i, a, ga = read_gates(*at(2, j), kLeastA);
-                    if (RESET && ((rst >> j) & 1)) ga = dup(0.0f);  // not used: whatever it holds
+                    if (rs) ga = dup(0.0f);  // not used: whatever it holds
                     sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r, i);
                     decays<EXACT, decltype(is_slow)::value>(mul2(k, r), em1[j], a);
                     float2 n = input_weight(em1[j]);
-                    if (RESET && ((rst >> j) & 1)) n = dup(1.0f);
+                    if (rs) n = dup(1.0f);
                     u[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
                 }
-            };
-            if (slow) form(std::true_type());
-            else form(std::false_type());
-            if (t + TPT > L) {  // tokens past the end change nothing
+                if (t + TPT > L) {  // tokens past the end change nothing
 #pragma unroll
-                for (int j = 0; j < TPT; ++j)
-                    if (t + j >= L) em1[j] = u[j] = dup(0.0f);
-            }
-            float2 A = dup(1.0f), H = dup(0.0f);
+                    for (int j = 0; j < TPT; ++j)
+                        if (t + j >= L) em1[j] = u[j] = dup(0.0f);
+                }
 #pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                const bool rs = RESET && ((rst >> j) & 1);
-                A = rs ? dup(0.0f) : fma2(em1[j], A, A);
-                H = rs ? u[j] : add2(H, fma2(em1[j], H, u[j]));
-            }
+                for (int j = 0; j < TPT; ++j) {
+                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
+                    A = rs ? dup(0.0f) : fma2(em1[j], A, A);
+                    H = rs ? u[j] : add2(H, fma2(em1[j], H, u[j]));
+                }
+            });
             ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
             if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
             __syncwarp();
@@ -447,11 +457,13 @@ __global__ void __launch_bounds__(kThreads, 3)
             // (a kept state's token starts a group)
             if (p.states && active && t < L && t % kInterval == 0)
                 *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
+            by_group<RESET>(true, rst, [&](auto, auto restarts) {
 #pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                h = RESET && ((rst >> j) & 1) ? u[j] : add2(h, fma2(em1[j], h, u[j]));
-                *at(2, j) = Pair<T>::narrow(h);
-            }
+                for (int j = 0; j < TPT; ++j) {
+                    h = decltype(restarts)::value && ((rst >> j) & 1) ? u[j] : add2(h, fma2(em1[j], h, u[j]));
+                    *at(2, j) = Pair<T>::narrow(h);
+                }
+            });
             tc::fence_smem_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
@@ -621,10 +633,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
             float2 r[TPT], i[TPT], em1[TPT];
             float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
-            auto form = [&](auto is_slow) {
+            by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
-                    const bool rs = RESET && ((rst >> j) & 1);
+                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
                     float2 a, ga = read_gates(*at(2, j), kLeastA);
                     if (rs) ga = dup(0.0f);
                     sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r[j], i[j]);
@@ -636,14 +648,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                     A = rs ? dup(0.0f) : fma2(em1[j], A, A);
                     H = rs ? u : add2(H, fma2(em1[j], H, u));
                 }
-            };
-            if (slow) form(std::true_type());
-            else form(std::false_type());
 #pragma unroll
-            for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
-                G = add2(G, Pair<T>::widen(*at(3, j)));
-                G = RESET && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
-            }
+                for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
+                    G = add2(G, Pair<T>::widen(*at(3, j)));
+                    G = decltype(restarts)::value && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
+                }
+            });
             ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
             ex.group_rev[warp][lane] = G;
             if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
@@ -657,20 +667,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int j = 0; j < TPT; ++j)
                 asm volatile("" : "+f"(em1[j].x), "+f"(em1[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
-            // forwards: the state before each token
+            by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
+                // forwards: the state before each token
 #pragma unroll
-            for (int j = 0; j < TPT; ++j) {
-                park(at(1, j), at(2, j), h);
-                const bool rs = RESET && ((rst >> j) & 1);
-                const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
-                const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                h = rs ? u : add2(h, fma2(em1[j], h, u));
-            }
-            // backwards: the outputs
-            auto back = [&](auto is_slow) {
+                for (int j = 0; j < TPT; ++j) {
+                    park(at(1, j), at(2, j), h);
+                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
+                    const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
+                    const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
+                    h = rs ? u : add2(h, fma2(em1[j], h, u));
+                }
+                // backwards: the outputs
 #pragma unroll
                 for (int j = TPT - 1; j >= 0; --j) {
-                    const bool rs = RESET && ((rst >> j) & 1);
+                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
                     const float2 x = Pair<T>::widen(*at(0, j)), hp = unpark(at(1, j), at(2, j));
                     g = add2(g, Pair<T>::widen(*at(3, j)));
                     const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
@@ -698,9 +708,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // two tokens at a time: all eight at once spill (388 us instead of 226)
                     if ((j & 1) == 0) asm volatile("" ::: "memory");
                 }
-            };
-            if (slow) back(std::true_type());
-            else back(std::false_type());
+            });
             tc::fence_smem_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
