@@ -140,7 +140,9 @@ __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& 
 
 // em1 = a - 1 = e^la - 1 (la <= 0) and a.  a = 1 + em1 enters the recurrence as
 // h + em1 h, so that a decay near 1 keeps its relative accuracy in la, and
-// 1 - a^2 = -em1 (2 + em1) without cancellation.  Down to -1/4 from the Taylor
+// 1 - a^2 = -em1 (2 + em1) without cancellation.  (The step rounds at 2^-24 of the
+// state before it, also where a small decay leaves little of that; a h + u
+// for such tokens, chosen token by token, made every call 3 % slower.)  Down to -1/4 from the Taylor
 // series to the sixth power (what it leaves out is below 2^-24 of em1), beyond
 // from e^la.  la never falls below the channel's own -scale softplus(decay),
 // so where that is above -1/4 (SLOW; the usual decays of 0.9 to 0.999 at the

@@ -14,6 +14,7 @@ from __future__ import annotations
 import numpy as np
 
 U = 2.0 ** -24
+TINY = 2.0 ** -126  # fp32 results below it may be zero
 D = 16 * U
 INTERVAL = 64
 
@@ -36,14 +37,15 @@ def softplus(v):
 
 
 def gates(gate_a, gate_x, decay, scale, reset):
-    """r, i, la, em1 = a - 1, n of every token; a = 0, n = 1 where reset."""
+    """r, i, la, a, em1 = a - 1, n of every token; a = 0, n = 1 where reset."""
     r, i = sigma(gate_a), sigma(gate_x)
     la = -scale * softplus(decay) * r
-    em1 = np.expm1(la)
+    a, em1 = np.exp(la), np.expm1(la)
     if reset is not None:
+        a = np.where((reset != 0)[..., None], 0.0, a)
         em1 = np.where((reset != 0)[..., None], -1.0, em1)
     n = np.sqrt(-em1 * (2.0 + em1))
-    return r, i, la, em1, n
+    return r, i, la, a, em1, n
 
 
 def gated_scan(x, gate_a, gate_x, decay, init=None, reset=None, scale=8.0):
@@ -51,7 +53,7 @@ def gated_scan(x, gate_a, gate_x, decay, init=None, reset=None, scale=8.0):
     x, gate_a, gate_x, decay = map(_np, (x, gate_a, gate_x, decay))
     init, reset = _np(init), _np(reset)
     b, L, C = x.shape
-    r, i, la, em1, n = gates(gate_a, gate_x, decay, scale, reset)
+    r, i, la, decays, em1, n = gates(gate_a, gate_x, decay, scale, reset)
     u = n * i * x
     h = np.zeros((b, C)) if init is None else init.copy()
     err = np.zeros((b, C))
@@ -61,12 +63,13 @@ def gated_scan(x, gate_a, gate_x, decay, init=None, reset=None, scale=8.0):
         if t % INTERVAL == 0:
             states.append(h.copy())
             e_states.append(err.copy())
-        a = 1.0 + em1[:, t]
-        keep = np.abs(a) > 0  # a restart forgets the state and its error exactly
+        a = decays[:, t]
+        keep = a > 0  # a restart forgets the state and its error exactly
         if reset is not None:
             keep = keep & (reset[:, t] == 0)[:, None]
         hn = np.where(keep, a * np.where(keep, h, 0.0), 0.0) + u[:, t]
-        # em1's own error, then four roundings of the new state
+        # h + em1 h: em1's own error and a rounding at the old state's size, however
+        # small a is; then four roundings of the new state
         err = np.where(keep, a * err + np.abs(em1[:, t] * np.where(keep, h, 0.0)) * D, 0.0) \
             + np.abs(u[:, t]) * D + 4 * U * np.abs(hn)
         h = hn
@@ -82,7 +85,7 @@ def gated_scan_bwd(x, gate_a, gate_x, decay, dy, init=None, reset=None, d_final=
     x, gate_a, gate_x, decay, dy = map(_np, (x, gate_a, gate_x, decay, dy))
     init, reset, d_final = _np(init), _np(reset), _np(d_final)
     b, L, C = x.shape
-    r, i, la, em1, n = gates(gate_a, gate_x, decay, scale, reset)
+    r, i, la, decays, em1, n = gates(gate_a, gate_x, decay, scale, reset)
     zero = np.zeros((b, C))
     hp = np.concatenate([(zero if init is None else init)[:, None], f["y"][:, :-1]], 1)
     e_hp = np.concatenate([zero[:, None], f["e_y"][:, :-1]], 1)
@@ -94,7 +97,9 @@ def gated_scan_bwd(x, gate_a, gate_x, decay, dy, init=None, reset=None, d_final=
         g = dy[:, t] + carry
         e_g = e_carry + 2 * U * np.abs(g)
         on = np.ones((b, 1), bool) if reset is None else (reset[:, t] == 0)[:, None]
-        a, nt, it = 1.0 + em1[:, t], n[:, t], i[:, t]
+        a, nt, it = decays[:, t], n[:, t], i[:, t]
+        # a = e^la with la off by D of itself: d(e^la) = a |la| D; and its own D
+        e_a = a * (1.0 + np.abs(la[:, t])) * D + TINY
         ix = it * x[:, t]
         o["dx"][:, t] = g * nt * it
         o["e_dx"][:, t] = e_g * np.abs(nt * it) + D * np.abs(o["dx"][:, t])
@@ -104,10 +109,12 @@ def gated_scan_bwd(x, gate_a, gate_x, decay, dy, init=None, reset=None, d_final=
                                 + D * np.abs(g * nt * ix))
         h_in = np.where(on, hp[:, t], 0.0)
         with np.errstate(divide="ignore", invalid="ignore"):
+            per_a = np.where(on & (nt > 0), a / np.where(nt > 0, nt, 1.0) * np.abs(ix), 0.0)
             w = np.where(on & (nt > 0), a * a / np.where(nt > 0, nt, 1.0) * ix, 0.0)
         dla = np.where(on, g * (a * h_in - w), 0.0)
         e_dla = np.where(on, e_g * np.abs(a * h_in - w)
-                         + np.abs(g) * (a * np.where(on, e_hp[:, t], 0.0) + D * (np.abs(a * h_in) + np.abs(w))), 0.0)
+                         + np.abs(g) * (a * np.where(on, e_hp[:, t], 0.0) + D * (np.abs(a * h_in) + np.abs(w))
+                                        + e_a * (np.abs(h_in) + 2.0 * per_a)), 0.0)
         k = la[:, t] * (1.0 - r[:, t])
         o["dgate_a"][:, t] = dla * k
         o["e_dgate_a"][:, t] = e_dla * np.abs(k) + D * np.abs(dla * la[:, t])

@@ -79,6 +79,26 @@ def test_gated_scan_and_gradient(case):
         within(o[k], ref[k], ref["e_" + k], k)
 
 
+@pytest.mark.parametrize("dtype,resets,scale,L", [(BF, 0, 0.25, 300), (BF, 6, 30.0, 700), (F32, 6, 30.0, 500),
+                                                  (F32, 0, 2.5, 130), (BF, 200, 8.0, 333)])
+def test_gated_scan_wide_decays(dtype, resets, scale, L):
+    """Channels that keep everything beside channels that keep nothing, other
+    scales, with and without restarts."""
+    d, dy, df = scan_inputs(2, L, 72, dtype, seed=L, resets=resets)
+    d["decay"] = torch.linspace(-9, 6, 72)[torch.randperm(72, generator=torch.Generator().manual_seed(1))]
+    g = dict(dev(d), scale=scale)
+    y, fin, st = ssd.ssd_gated_scan(**g, return_final_state=True, return_states=True)
+    a = (d["x"], d["gate_a"], d["gate_x"], d["decay"])
+    ref = om.gated_scan(*a, d["init_state"], d["reset"], scale=scale)
+    within(y, ref["y"], ref["e_y"], "y")
+    within(fin, ref["final"], ref["e_final"], "final_state")
+    g.pop("init_state")
+    o = ssd.ssd_gated_scan_bwd(dy=dy.to(DEV), states=st, d_final=df.to(DEV), **g)
+    ref = om.gated_scan_bwd(*a, dy, d["init_state"], d["reset"], df, scale=scale)
+    for k in ("dx", "dgate_a", "dgate_x", "ddecay", "d_init"):
+        within(o[k], ref[k], ref["e_" + k], k)
+
+
 def test_gated_scan_extreme_gates_and_decays():
     """Open and shut gates, decays of 1 and 0 and everything between, in both types."""
     vals = torch.tensor([-200.0, -30.0, -8.0, -1.0, 0.0, 1.0, 8.0, 30.0, 200.0])
@@ -347,6 +367,39 @@ def test_norm_rope_without_weights_and_zero_heads():
     e = torch.ones_like(z)
     g = ssd.ssd_qk_norm_rope_bwd(z, None, None, None, f, e, None)
     assert torch.allclose(g["dq"], e / (1e-5 ** 0.5), rtol=1e-6) and (g["dq_weight"] == 0).all()
+
+
+def test_norm_rope_negative_and_repeated_positions_and_high_frequencies():
+    """Positions below zero, the same one twice, and more than a turn per position.
+    The turns per position are off by up to 2^-53 of themselves (fp64) and 2^-65
+    (the fraction), the angle in turns by that times |position|."""
+    b, L, h, D, R = 1, 8, 2, 64, 32
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn((b, L, h, D), generator=g).to(DEV)
+    f = (torch.linspace(-7.5, 7.5, R // 2)).to(DEV)
+    pos = torch.tensor([[-1, -70000, 5, 5, 0, -(1 << 20), 1 << 20, 3]]).to(DEV)
+    turns = f.double().abs().max().item() / 6.28 * (1 << 20) * 2.0 ** -53 + (1 << 20) * 2.0 ** -65
+    out, _ = ssd.ssd_qk_norm_rope(q, None, None, None, f, pos)
+    ref, err = om.norm_rope(q, None, f, pos, eps=1e-5, adjacent=False)
+    size = np.abs(om.norm_rope(q, None, None, None, eps=1e-5, adjacent=False)[0]).max()
+    within(out, ref, err + 6.3 * turns * 2 * size, "out")
+    assert torch.equal(ssd.ssd_qk_norm_rope(q[:, 2:4], None, None, None, f, pos[:, 2:4].contiguous())[0],
+                       out[:, 2:4])
+
+
+def test_norm_rope_nan_stays_in_its_head():
+    q = torch.randn((2, 33, 5, 128), generator=torch.Generator().manual_seed(9)).to(BF).to(DEV)
+    f = (10000.0 ** (-torch.arange(0, 128, 2) / 128)).to(DEV)
+    dirty = q.clone()
+    dirty[1, 7, 3, 100] = float("nan")
+    dirty[0, 20, 0, 0] = float("inf")
+    keep = torch.ones((2, 33, 5), dtype=torch.bool, device=DEV)
+    keep[1, 7, 3] = keep[0, 20, 0] = False
+    a, b = (ssd.ssd_qk_norm_rope(t, None, None, None, f)[0] for t in (q, dirty))
+    assert torch.equal(a[keep], b[keep]) and torch.isnan(b[1, 7, 3]).all()
+    e = torch.randn_like(q)
+    a, b = (ssd.ssd_qk_norm_rope_bwd(t, None, None, None, f, e, None)["dq"] for t in (q, dirty))
+    assert torch.equal(a[keep], b[keep])
 
 
 # ---- the convolution's gradient ---------------------------------------------
