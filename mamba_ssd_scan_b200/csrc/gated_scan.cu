@@ -142,20 +142,20 @@ __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& 
 // h + em1 h, so that a decay near 1 keeps its relative accuracy in la, and
 // 1 - a^2 = -em1 (2 + em1) without cancellation.  (The step rounds at 2^-24 of the
 // state before it, also where a small decay leaves little of that; a h + u
-// for such tokens, chosen token by token, made every call 3 % slower.)  Down to -1/4 from the Taylor
-// series to the sixth power (what it leaves out is below 2^-24 of em1), beyond
-// from e^la.  la never falls below the channel's own -scale softplus(decay),
-// so where that is above -1/4 (SLOW; the usual decays of 0.9 to 0.999 at the
-// open gate) the second form is not evaluated.  The choice is made once per
-// group, not per token: a branch between the tokens kept them from overlapping
-// (220 cycles per token and warp).
+// for such tokens, chosen token by token, made every call 3 % slower.)
+// Down to -1/4 em1 = la + la^2 q, q the cubic that is nearest to
+// (e^la - 1 - la) / la^2 there by em1's relative error (fitted: off by 2^-28 of
+// em1; the series needs another term), beyond from e^la.  la never falls below
+// the channel's own -scale softplus(decay), so where that is above -1/4 (SLOW; the
+// usual decays of 0.9 to 0.999 at the open gate) the second form is not
+// evaluated.  The choice is made once per group, not per token: a branch between
+// the tokens kept them from overlapping (220 cycles per token and warp).
 template <bool EXACT, bool SLOW>
 __device__ __forceinline__ void decays(float2 la, float2& em1, float2& a) {
-    float2 q = dup(1.0f / 720.0f);
-    q = fma2(q, la, dup(1.0f / 120.0f));
-    q = fma2(q, la, dup(1.0f / 24.0f));
-    q = fma2(q, la, dup(1.0f / 6.0f));
-    q = fma2(q, la, dup(0.5f));
+    float2 q = dup(0.0075347102f);
+    q = fma2(q, la, dup(0.041502319f));
+    q = fma2(q, la, dup(0.16665322f));
+    q = fma2(q, la, dup(0.49999964f));
     em1 = fma2(mul2(q, la), la, la);
     a = add2(em1, dup(1.0f));
     if constexpr (!SLOW) {
