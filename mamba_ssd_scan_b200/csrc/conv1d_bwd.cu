@@ -222,10 +222,11 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
     if (!ok) atomicExch(&g_conv_bwd_status, static_cast<int>(SSD_ERR_TIMEOUT));
 }
 
-__global__ void __launch_bounds__(kColSumThreads) conv1d_bwd_finish_kernel(ConvBwdParams p, int64_t rows) {
+constexpr int kSumWarps = 8;
+__global__ void __launch_bounds__(kSumWarps * 32) conv1d_bwd_finish_kernel(ConvBwdParams p, int64_t rows) {
     grid_dep_wait();
     const int64_t K = p.width, Cn = p.channels;
-    column_sums(p.partial, rows, (K + 1) * Cn, [&](int64_t i, float s) {
+    column_sums<kSumWarps>(p.partial, rows, (K + 1) * Cn, [&](int64_t i, float s) {
         const int64_t k = i / Cn, c = i - k * Cn;
         if (k < K) p.dweight[c * K + k] = s;
         else if (p.dbias) p.dbias[c] = s;
@@ -278,7 +279,7 @@ template <typename T, int K> cudaError_t launch_k(const ConvBwdParams& p, cudaSt
     if (e != cudaSuccess) return e;
     const int64_t cols = (p.width + 1) * p.channels;
     return launch_kernel(conv1d_bwd_finish_kernel, dim3(static_cast<unsigned>((cols + 31) / 32)),
-                         dim3(kColSumThreads), 0, s, true, p, p.batch * g.nseg);
+                         dim3(kSumWarps * 32), 0, s, true, p, p.batch * g.nseg);
 }
 
 }  // namespace

@@ -731,9 +731,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // ddecay = -scale * sigma(decay) * the sum of dla * r over batch and time
-__global__ void __launch_bounds__(kColSumThreads) gated_scan_finish_kernel(GatedScanParams p, int64_t rows) {
+constexpr int kSumWarps = 8;
+__global__ void __launch_bounds__(kSumWarps * 32) gated_scan_finish_kernel(GatedScanParams p, int64_t rows) {
     grid_dep_wait();
-    column_sums(p.partial, rows, p.channels, [&](int64_t c, float s) {
+    column_sums<kSumWarps>(p.partial, rows, p.channels, [&](int64_t c, float s) {
         p.ddecay[c] = -p.scale * sigma_f32(p.decay[c]) * s;
     });
 }
@@ -935,7 +936,7 @@ template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p
                 : launch_clusters<gated_scan_bwd_kernel<T, false>>(p, TILE, smem, s, &cl, m);
     if (e != cudaSuccess) return e;
     return launch_kernel(gated_scan_finish_kernel, dim3(static_cast<unsigned>((p.channels + 31) / 32)),
-                         dim3(kColSumThreads), 0, s, true, p, p.batch * cl);
+                         dim3(kSumWarps * 32), 0, s, true, p, p.batch * cl);
 }
 
 template <typename T, int R> cudaError_t launch_update_rows(const GatedUpdateParams& p, cudaStream_t s) {

@@ -475,12 +475,13 @@ __global__ void __launch_bounds__(TPB, 2)
     }
 }
 
-__global__ void __launch_bounds__(kColSumThreads)
+constexpr int kSumWarps = 32;  // (up to 296 rows of few columns: 8 warps 7.7 us, 32 6)
+__global__ void __launch_bounds__(kSumWarps * 32)
     norm_rope_finish_kernel(NormRopeParams p, int64_t rows_q, int64_t rows_k) {
     grid_dep_wait();
     const int kd = blockIdx.y;
     if (!p.dweight[kd]) return;
-    column_sums(p.partial[kd], kd ? rows_k : rows_q, p.headdim,
+    column_sums<kSumWarps>(p.partial[kd], kd ? rows_k : rows_q, p.headdim,
                 [&](int64_t c, float s) { p.dweight[kd][c] = s; });
 }
 
@@ -575,7 +576,7 @@ template <typename T, int LPU> cudaError_t launch_bwd(const NormRopeParams& p, c
     if (e != cudaSuccess || (!p.dweight[0] && !p.dweight[1])) return e;
     return launch_kernel(norm_rope_finish_kernel,
                          dim3(static_cast<unsigned>((p.headdim + 31) / 32), ck > 0 ? 2 : 1),
-                         dim3(kColSumThreads), 0, s, true, p, cq, ck);
+                         dim3(kSumWarps * 32), 0, s, true, p, cq, ck);
 }
 
 template <typename T, bool BWD> cudaError_t launch(const NormRopeParams& p, cudaStream_t s) {

@@ -61,30 +61,29 @@ template <> struct Pair<__nv_bfloat16> {
 };
 
 // Sums of the columns of partial [rows][cols] (fp32), rows in a fixed order:
-// a block takes 32 columns, its 8 warps every 8th row each, and the warps'
-// sums are added in order.  The value of column c goes to store(c, sum).
-constexpr int kColSumThreads = 256;
-template <typename Store>
+// a block takes 32 columns, its W warps every W-th row each, and the warps' sums
+// are added in order.  The value of column c goes to store(c, sum).
+template <int W, typename Store>
 __device__ __forceinline__ void column_sums(const float* partial, int64_t rows, int64_t cols, Store store) {
-    __shared__ float part[kColSumThreads / 32][32];
+    __shared__ float part[W][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
     float s = 0.0f;
     if (c < cols) {
         int64_t r = warp;
-        for (; r + 24 < rows; r += 32) {  // four loads in flight
-            const float a = partial[r * cols + c], b = partial[(r + 8) * cols + c];
-            const float d = partial[(r + 16) * cols + c], e = partial[(r + 24) * cols + c];
+        for (; r + 3 * W < rows; r += 4 * W) {  // four loads in flight
+            const float a = partial[r * cols + c], b = partial[(r + W) * cols + c];
+            const float d = partial[(r + 2 * W) * cols + c], e = partial[(r + 3 * W) * cols + c];
             s += (a + b) + (d + e);
         }
-        for (; r < rows; r += 8) s += partial[r * cols + c];
+        for (; r < rows; r += W) s += partial[r * cols + c];
     }
     part[warp][lane] = s;
     __syncthreads();
     if (warp == 0 && c < cols) {
         float t = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kColSumThreads / 32; ++w) t += part[w][lane];
+        for (int w = 0; w < W; ++w) t += part[w][lane];
         store(c, t);
     }
 }
