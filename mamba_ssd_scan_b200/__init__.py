@@ -916,7 +916,7 @@ def ssd_causal_conv1d_bwd(x, weight, dy, bias=None, init_state=None, d_final=Non
     x, dy [b,L,C] in one dtype; weight [C,K], bias [C], init_state and d_final
     [b,C,K-1] float32 (the last three optional).  Returns a dict dx (x's dtype),
     dweight [C,K], dbias [C], d_init [b,C,K-1] (float32); ``out`` may hold
-    preallocated tensors under the same keys."""
+    preallocated tensors under the same keys; dx must not overlap x or dy."""
     entry = _entry("ssd_causal_conv1d_bwd", SsdConv1dBwdArgs)
     shape, dt, dev = x.shape, x.dtype, x.get_device()
     b, L, Cn = shape
@@ -952,7 +952,7 @@ def ssd_gated_scan(x, gate_a, gate_x, decay, init_state=None, reset=None, *, sca
     [b,C] float32; reset [b,L] bool or uint8, nonzero where a token starts a new
     sequence.  Returns y, then the final state [b,C] and the states entering
     every 64th token [b,ceil(L/64),C] (for ssd_gated_scan_bwd), each when asked
-    for or given."""
+    for or given.  Outputs must not overlap inputs."""
     entry = _entry("ssd_gated_scan", SsdGatedScanArgs)
     shape, dt, dev = x.shape, x.dtype, x.get_device()
     b, L, Cn = shape
@@ -993,7 +993,7 @@ def ssd_gated_scan_bwd(x, gate_a, gate_x, decay, dy, states, reset=None, d_final
     ``states`` is what the forward returned with return_states for the same
     inputs.  Returns a dict dx, dgate_a, dgate_x (x's dtype), ddecay [C] and
     d_init [b,C] (float32); ``out`` may hold preallocated tensors under the same
-    keys."""
+    keys, which must not overlap inputs."""
     entry = _entry("ssd_gated_scan_bwd", SsdGatedScanBwdArgs)
     shape, dt, dev = x.shape, x.dtype, x.get_device()
     b, L, Cn = shape
@@ -1117,7 +1117,7 @@ def ssd_qk_norm_rope_bwd(q, k, q_weight, k_weight, inv_freq, dq_out, dk_out, pos
     and k's shapes, dense or slices as there).  Returns a dict dq, dk (q's dtype;
     dk absent without k), dq_weight, dk_weight [D] (float32); ``out`` may hold
     preallocated tensors under the same keys, dq and dk also as slices of packed
-    rows."""
+    rows; they must not overlap inputs."""
     entry = _entry("ssd_qk_norm_rope_bwd", SsdQkNormRopeBwdArgs)
     qs, dt, dev = q.shape, q.dtype, q.get_device()
     b, L, hq, D = qs

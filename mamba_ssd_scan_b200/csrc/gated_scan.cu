@@ -21,11 +21,13 @@
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
 //
 // Measured (B200, L2 flushed; share of the measured copy bandwidth over the
-// call's least bytes).  Forward, bf16: b6 L4096 C4736 176 us (82 %), b8 L4096
-// C2048 129 us (65 %), b1 L65536 C1536 229 us (55 %); fp32: b8 L4096 C2048 200
-// us (83 %).  Gradient, bf16: b4 L4096 C4736 228 us (74 %), b8 L4096 C2048 226
-// us (65 %), b1 L65536 C1536 425 us (52 %).  Where the CTAs fill the SMs evenly
-// the forward is bound by its instructions (57 per channel pair and token; issue
+// call's least bytes).  Forward, bf16: b6 L4096 C4736 172 us (84 %), b8 L4096
+// C2048 127 us (66 %), with restarts 145; b1 L65536 C1536 227 us (55 %); fp32: b8
+// L4096 C2048 197 us (85 %).  Gradient, bf16: b4 L4096 C4736 225 us (75 %), b8
+// L4096 C2048 223 us (65 %), with restarts 250; b1 L65536 C1536 421 us (52 %).
+// Groups of 16 tokens at two CTAs per SM measured 220 us at b6 C4736, groups of
+// four at four CTAs 203.  Where the CTAs fill the SMs evenly the
+// forward is bound by its instructions (55 per channel pair and token; issue
 // slots 55 % busy, the special-function pipe 62 %) as much as by its bytes, and
 // the gradient by its own (issue 54 %, FMA pipe 46 %, at two CTAs per SM).  b8 C2048
 // is 256 CTAs on 148 SMs, a third of which take one where the others take two;

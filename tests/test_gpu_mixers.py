@@ -661,3 +661,98 @@ def test_nothing_outside_the_outputs_is_written():
     torch.cuda.synchronize()
     for buf, end in bands:
         assert (buf[:512] == 0xA5).all() and (buf[end:] == 0xA5).all()
+
+
+def test_largest_batches_and_head_counts():
+    """The limits of the grid: the last batch row or head alone gives the same."""
+    b = 65535
+    g = torch.Generator(device=DEV).manual_seed(2)
+    x, ga, gx, dy = (torch.randn((b, 2, 8), generator=g, device=DEV).to(BF) for _ in range(4))
+    dec = torch.linspace(-6, 1, 8, device=DEV)
+    one = [t[-1:].clone() for t in (x, ga, gx)]
+    y, fin, st = ssd.ssd_gated_scan(x, ga, gx, dec, return_final_state=True, return_states=True)
+    y1, fin1, st1 = ssd.ssd_gated_scan(*one, dec, return_final_state=True, return_states=True)
+    assert torch.equal(y[-1:], y1) and torch.equal(fin[-1:], fin1)
+    o = ssd.ssd_gated_scan_bwd(x, ga, gx, dec, dy, st)
+    o1 = ssd.ssd_gated_scan_bwd(*one, dec, dy[-1:].clone(), st1)
+    assert all(torch.equal(o[k][-1:], o1[k]) for k in ("dx", "dgate_a", "dgate_x", "d_init"))
+    s, s1 = fin.clone(), fin[-1:].clone()
+    y = ssd.ssd_gated_state_update(s, *(t[:, 0].contiguous() for t in (x, ga, gx)), dec)
+    y1 = ssd.ssd_gated_state_update(s1, *(t[:, 0].contiguous() for t in one), dec)
+    assert torch.equal(y[-1:], y1) and torch.equal(s[-1:], s1)
+    w = torch.randn((8, 4), generator=g, device=DEV)
+    c = ssd.ssd_causal_conv1d_bwd(x, w, dy)
+    c1 = ssd.ssd_causal_conv1d_bwd(one[0], w, dy[-1:].clone())
+    assert torch.equal(c["dx"][-1:], c1["dx"]) and torch.equal(c["d_init"][-1:], c1["d_init"])
+    q = torch.randn((1, 2, 65535, 16), generator=g, device=DEV).to(BF)
+    k = torch.randn((1, 2, 1, 16), generator=g, device=DEV).to(BF)
+    f = torch.rand(8, generator=g, device=DEV)
+    qo, ko = ssd.ssd_qk_norm_rope(q, k, None, None, f)
+    q1, k1 = ssd.ssd_qk_norm_rope(q[:, :, -1:].contiguous(), k, None, None, f)
+    assert torch.equal(qo[:, :, -1:], q1) and torch.equal(ko, k1)
+    g2 = ssd.ssd_qk_norm_rope_bwd(q, k, None, None, f, qo, ko)
+    g1 = ssd.ssd_qk_norm_rope_bwd(q[:, :, -1:].contiguous(), k, None, None, f, q1, k1)
+    assert torch.equal(g2["dq"][:, :, -1:], g1["dq"]) and torch.equal(g2["dk"], g1["dk"])
+
+
+def test_calls_from_several_threads():
+    """Host threads with a stream each, at the same time."""
+    import threading
+    fns = [_calls(s) for s in (1, 2, 3, 4)]
+    want = [[fn() for fn in row] for row in fns]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(row, refs):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                outs = [fn() for fn in row]
+                s.synchronize()
+                bad.extend(i for i, (a, b) in enumerate(zip(outs, refs))
+                           if not all(torch.equal(p, q) for p, q in zip(a, b)))
+    threads = [threading.Thread(target=work, args=a) for a in zip(fns, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+FIRST_CALLS = r"""
+import sys, torch
+sys.path.insert(0, ROOT)
+import mamba_ssd_scan_b200 as ssd
+g = torch.Generator(device="cuda").manual_seed(0)
+rn = lambda *s: torch.randn(s, generator=g, device="cuda")
+x, ga, gx, dy = (rn(2, 300, 64).bfloat16() for _ in range(4))
+dec, q, f, w = torch.full((64,), -4.0, device="cuda"), rn(2, 9, 4, 64).bfloat16(), rn(32), rn(64, 4)
+st, s0 = torch.zeros(2, 5, 64, device="cuda"), torch.zeros(2, 64, device="cuda")
+one = [t[:, 0].contiguous() for t in (x, ga, gx)]
+for run in (lambda: [ssd.ssd_gated_scan(x, ga, gx, dec)],
+            lambda: list(ssd.ssd_gated_scan_bwd(x, ga, gx, dec, dy, st).values()),
+            lambda: [ssd.ssd_gated_state_update(s0, *one, dec, new_state=torch.empty_like(s0))],
+            lambda: [ssd.ssd_qk_norm_rope(q, None, None, None, f)[0]],
+            lambda: list(ssd.ssd_qk_norm_rope_bwd(q, None, None, None, f, q, None).values()),
+            lambda: list(ssd.ssd_causal_conv1d_bwd(x, w, dy).values())):
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    graph.replay()
+    torch.cuda.synchronize()
+    again = run()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, again))
+print("CAPTURE-OK")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", f"ROOT = {root!r}\n" + FIRST_CALLS], capture_output=True, text=True,
+                       timeout=180)
+    assert r.returncode == 0 and "CAPTURE-OK" in r.stdout, r.stdout + r.stderr
