@@ -262,8 +262,9 @@ cudaError_t launch_act(const ConvBwdParams& p, const ConvBwdMaps& m, const ConvG
     constexpr int smem = NW * kWarpBytes<T>;
     const cudaError_t e = prepare_kernel<conv1d_bwd_kernel<T, K, ACT>>(smem, false);
     if (e != cudaSuccess) return e;
-    conv1d_bwd_kernel<T, K, ACT><<<static_cast<unsigned>((g.warps + NW - 1) / NW), NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg),
-                                                                             g.warps);
+    const auto ctas = static_cast<unsigned>((g.warps + NW - 1) / NW);
+    conv1d_bwd_kernel<T, K, ACT>
+        <<<ctas, NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg), g.warps);
     return cudaGetLastError();
 }
 

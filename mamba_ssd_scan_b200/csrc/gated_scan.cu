@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 3)
                     const float2 aa = gr ? dup(0.0f) : mul2(make_float2(g[w].x, g[w].y), make_float2(m.x, m.y));
                     m = make_float4(aa.x, aa.y, hh.x, hh.y);
                 }
-                ok = exchange_tiles<RESET>(ex, m, rst != 0, it, rank, cl, rank == 0 && it == withhold, tile_bytes, lane);
+                ok = exchange_tiles<RESET>(ex, m, rst != 0, it, rank, cl, rank == 0 && it == withhold, tile_bytes,
+                                           lane);
                 for (int q = 0; q < cl; ++q) {
                     if (q == rank) h = carry;
                     carry = apply(ex.tile_map[buf][q][lane], RESET && ex.tile_rst[buf][q], carry);
@@ -531,7 +532,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     init_exchange(ex);
     if (cl > 1) cluster_sync_all();
     // rounds run backwards: the first token of this CTA's tile
-    auto first = [&](int it) { return static_cast<int64_t>(rounds - 1 - it) * round + static_cast<int64_t>(rank) * TILE; };
+    auto first = [&](int it) {
+        return static_cast<int64_t>(rounds - 1 - it) * round + static_cast<int64_t>(rank) * TILE;
+    };
     float2 sum = dup(0.0f);
 
     if (warp == NW) {
@@ -670,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             // of the group would cost 32 more registers.
 #pragma unroll
             for (int j = 0; j < TPT; ++j)
-                asm volatile("" : "+f"(em1[j].x), "+f"(em1[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
+                asm volatile(""
+                             : "+f"(em1[j].x), "+f"(em1[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
             by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
                 // forwards: the state before each token
 #pragma unroll

@@ -118,7 +118,8 @@ template <int N> struct Angles {
             own += tstep;
             while (own >= len) own -= len;
             const int64_t part = static_cast<int64_t>(static_cast<uint64_t>(pos) * static_cast<uint64_t>(turn));
-            const float2 v = cos_sin_turn(static_cast<float>(static_cast<int32_t>(part >> 32)) * 2.3283064365386963e-10f);
+            const float f = static_cast<float>(static_cast<int32_t>(part >> 32)) * 2.3283064365386963e-10f;  // 2^-32
+            const float2 v = cos_sin_turn(f);
             float* c = reinterpret_cast<float*>(cs) + t * p.rot_dim + place;
             c[0] = v.x;
             c[2] = v.y;
