@@ -2,8 +2,9 @@
 // formulas stand in include/ssd.h).
 //
 // Bandwidth-bound: x and dy are read once and dx written once.  A warp takes 64
-// channels (a pair per lane) over a segment of the sequence, in batches of 8
-// tokens that TMA brings into its own ring of shared-memory tiles.  It keeps
+// channels (a pair per lane) over a segment of the sequence, in batches of 16
+// tokens (8 of fp32) that TMA brings into its own ring of shared-memory tiles.
+// It takes eight tokens of a batch at a time and keeps
 // two windows in registers: the K inputs that feed a token's output, and the
 // last K gradients before the activation, whose weighted sum is the gradient
 // of the input K - 1 tokens back.  dx takes the place of x in the tile and
@@ -15,9 +16,9 @@
 // kernel adds the rows in order.
 //
 // Measured (B200, L2 flushed; share of the measured copy bandwidth over the
-// call's least bytes), K 4 with SiLU: bf16 b1 L65536 C5376 388 us (84 %), b8 L4096
-// C2304 100 us (71 %); fp32 b8 L4096 C1536 114 us (82 %).  A segment costs 0.16
-// us per token and about 12 us for its start, its end and the sums; issue slots
+// call's least bytes), K 4 with SiLU: bf16 b1 L65536 C5376 373 us (88 %), b8 L4096
+// C2304 96 us (73 %); fp32 b8 L4096 C1536 115 us (82 %).  A segment costs 0.15
+// us per token and about 17 us for its start, its end and the sums; issue slots
 // are 57 % busy (48 instructions per channel pair and token), the FMA pipe 51 %,
 // the special-function pipe 39 %.
 #include "mixers.h"
@@ -30,14 +31,18 @@ namespace {
 
 constexpr int NW = 8;     // warps (segments) per CTA
 constexpr int CPW = 64;   // channels per warp
-constexpr int TB = 8;     // tokens per batch (at least K - 1)
+constexpr int SB = 8;     // tokens at a time (at least K - 1)
+// Tokens per batch: tiles of 2 KB.  Of half that (8 tokens of bf16) the TMA
+// requests are twice as many, b1 L65536 C5376 K4 took 394 us instead of 372.
+template <typename T> constexpr int kBatch = sizeof(T) == 2 ? 16 : 8;
+constexpr int kSegUnit = 16;  // segments are whole batches of either type
 // CTAs per SM: two, whose 128 registers a thread let the tokens of a batch overlap
-// (b8 L4096 C2304 K4: 100 us; three at 80 registers 109, four at 64 130; windows
-// of four tokens instead of eight, two CTAs 108, three 112)
+// (b8 L4096 C2304 K4, batches of 8: 100 us; three at 80 registers 109, four at 64
+// 130; windows of four tokens instead of eight, two CTAs 108, three 112)
 constexpr int kPerSm = 2;
-template <typename T> constexpr int kRing = sizeof(T) == 2 ? 4 : 3;          // batches in shared memory
+constexpr int kRing = 3;  // batches in shared memory
 template <typename T> constexpr int kRowBytes = CPW * sizeof(T);
-template <typename T> constexpr int kWarpBytes = kRing<T> * 2 * TB * kRowBytes<T>;  // x and dy tiles
+template <typename T> constexpr int kWarpBytes = kRing * 2 * kBatch<T> * kRowBytes<T>;  // x and dy tiles
 
 // SSD_ERR_TIMEOUT once a launch gave up on a wait; read and cleared by
 // ssd_conv1d_check_status.
@@ -70,13 +75,13 @@ struct ConvBwdMaps {
     CUtensorMap x, dy, dx;
 };
 
-// segments of seg tokens (a multiple of TB), nseg per (batch, channel block)
+// segments of seg tokens (a multiple of kSegUnit), nseg per (batch, channel block)
 template <typename T, int K, bool ACT>
 __global__ void __launch_bounds__(NW * 32, kPerSm)
     conv1d_bwd_kernel(ConvBwdParams p, const __grid_constant__ ConvBwdMaps maps, int64_t seg, int nseg, int64_t warps) {
     using P = Pair<T>;
     using Raw = typename P::Raw;
-    constexpr int R = kRing<T>, KM = K - 1;
+    constexpr int R = kRing, KM = K - 1, TB = kBatch<T>;
     constexpr uint32_t kTile = TB * kRowBytes<T>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t loaded[NW][R];
@@ -118,9 +123,9 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
     if (active && p.bias) bias = make_float2(p.bias[c], p.bias[c + 1]);
     const T* xb = static_cast<const T*>(p.x) + b * L * Cn + c;
     T* dxb = static_cast<T*>(p.dx) + b * L * Cn + c;
-    // xw[KM + j]: the input of batch token j; xw[0 .. KM - 1] the K - 1 before.
+    // xw[KM + j]: the input of token j of the eight; xw[0 .. KM - 1] the K - 1 before.
     // dv alike: the gradients before the activation.
-    float2 xw[KM + TB], dv[KM + TB];
+    float2 xw[KM + SB], dv[KM + SB];
 #pragma unroll
     for (int k = 0; k < KM; ++k) {
         dv[k] = dup(0.0f);
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
             xw[k] = make_float2(p.init_state[(b * Cn + c) * KM + (KM + i)],
                                 p.init_state[(b * Cn + c + 1) * KM + (KM + i)]);
     }
-    // token j of a batch: its input and its gradient before the activation
+    // token j of eight: its input and its gradient before the activation
     auto token = [&](const uint8_t* tile, int j) {
         xw[KM + j] = P::widen(*reinterpret_cast<const Raw*>(tile + j * kRowBytes<T>));
         float2 d = P::widen(*reinterpret_cast<const Raw*>(tile + kTile + j * kRowBytes<T>));
@@ -161,46 +166,50 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         const int64_t t0 = ta + static_cast<int64_t>(n) * TB;
         const bool halo = n == nb;
         ok &= tc::mbar_wait(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
-        if (n > 0 && !halo && t0 + TB <= L) {  // whole batches inside the segment, without a condition
+        const bool whole = n > 0 && !halo && t0 + TB <= L;  // inside the segment, without a condition
+#pragma unroll 1
+        for (int o = 0; o < (halo ? SB : TB); o += SB, tile += SB * kRowBytes<T>) {
+            if (whole) {
 #pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                token(tile, j);
-                sums(j);
-                *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(input_gradient(j));
-            }
-            tc::fence_smem_async();
-        } else {
-#pragma unroll
-            for (int j = 0; j < TB; ++j) {
-                token(tile, j);
-                // no gradient past the sequence's end, whatever the inputs before it
-                if (t0 + j >= L) dv[KM + j] = dup(0.0f);
-                if (!halo) sums(j);
-                float2 g = input_gradient(j);
-                const int64_t f = t0 + j - L;
-                if (f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
-                    g.x += p.d_final[(b * Cn + c) * KM + f];
-                    g.y += p.d_final[(b * Cn + c + 1) * KM + f];
+                for (int j = 0; j < SB; ++j) {
+                    token(tile, j);
+                    sums(j);
+                    *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(input_gradient(j));
                 }
-                const int64_t i = t0 + j - KM;
-                if (n > 0 && !halo) {
-                    *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g);
-                } else if (active) {
-                    if (halo ? (j < KM && i < te) : i >= ta) {
-                        if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g);
-                    } else if (n == 0 && i < 0 && p.d_init) {
-                        p.d_init[(b * Cn + c) * KM + (KM + i)] = g.x;
-                        p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g.y;
+            } else {
+                const int64_t t = t0 + o;
+#pragma unroll
+                for (int j = 0; j < SB; ++j) {
+                    token(tile, j);
+                    // no gradient past the sequence's end, whatever the inputs before it
+                    if (t + j >= L) dv[KM + j] = dup(0.0f);
+                    if (!halo) sums(j);
+                    float2 g = input_gradient(j);
+                    const int64_t f = t + j - L;
+                    if (f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
+                        g.x += p.d_final[(b * Cn + c) * KM + f];
+                        g.y += p.d_final[(b * Cn + c + 1) * KM + f];
+                    }
+                    const int64_t i = t + j - KM;
+                    if (n > 0 && !halo) {
+                        *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g);
+                    } else if (active) {
+                        if (halo ? (j < KM && i < te) : i >= ta) {
+                            if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g);
+                        } else if (n == 0 && i < 0 && p.d_init) {
+                            p.d_init[(b * Cn + c) * KM + (KM + i)] = g.x;
+                            p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g.y;
+                        }
                     }
                 }
             }
-            if (n > 0 && !halo) tc::fence_smem_async();
-        }
 #pragma unroll
-        for (int k = 0; k < KM; ++k) {
-            xw[k] = xw[TB + k];
-            dv[k] = dv[TB + k];
+            for (int k = 0; k < KM; ++k) {
+                xw[k] = xw[SB + k];
+                dv[k] = dv[SB + k];
+            }
         }
+        if (n > 0 && !halo) tc::fence_smem_async();
         __syncwarp();
         if (lane == 0) {
             if (n > 0 && !halo) {
@@ -245,7 +254,7 @@ ConvGrid conv_grid(int64_t batch, int64_t seqlen, int64_t channels) {
     int64_t least = 0;
     for (int64_t n = 1; n <= 1024 && (n == 1 || (seqlen + n - 1) / n >= 32); ++n) {
         ConvGrid g;
-        g.seg = ((seqlen + n - 1) / n + TB - 1) / TB * TB;
+        g.seg = ((seqlen + n - 1) / n + kSegUnit - 1) / kSegUnit * kSegUnit;
         g.nseg = (seqlen + g.seg - 1) / g.seg;
         g.warps = cols * g.nseg;
         const int64_t cost = (g.warps + slots - 1) / slots * (g.seg + 16);
@@ -272,9 +281,9 @@ template <typename T, int K> cudaError_t launch_k(const ConvBwdParams& p, cudaSt
     const ConvGrid g = conv_grid(p.batch, p.seqlen, p.channels);
     ConvBwdMaps m;
     const bool bf16 = sizeof(T) == 2;
-    if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, TB) ||
-        !make_tmap_rows(&m.dy, p.dy, bf16, p.channels, p.seqlen, p.batch, TB) ||
-        !make_tmap_rows(&m.dx, p.dx, bf16, p.channels, p.seqlen, p.batch, TB))
+    if (!make_tmap_rows(&m.x, p.x, bf16, p.channels, p.seqlen, p.batch, kBatch<T>) ||
+        !make_tmap_rows(&m.dy, p.dy, bf16, p.channels, p.seqlen, p.batch, kBatch<T>) ||
+        !make_tmap_rows(&m.dx, p.dx, bf16, p.channels, p.seqlen, p.batch, kBatch<T>))
         return cudaErrorInvalidValue;
     const cudaError_t e = p.activation ? launch_act<T, K, true>(p, m, g, s) : launch_act<T, K, false>(p, m, g, s);
     if (e != cudaSuccess) return e;
