@@ -181,9 +181,10 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
 #pragma unroll
                 for (int j = 0; j < SB; ++j) {
                     token(tile, j);
-                    // no gradient past the sequence's end, whatever the inputs before it
+                    // no gradient past the sequence's end, whatever the inputs before it, and no
+                    // share of the sums (0 times an infinite input is not 0)
                     if (t + j >= L) dv[KM + j] = dup(0.0f);
-                    if (!halo) sums(j);
+                    else if (!halo) sums(j);
                     float2 g = input_gradient(j);
                     const int64_t f = t + j - L;
                     if (f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
