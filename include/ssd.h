@@ -515,7 +515,10 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
  *   channels] fp32 or NULL: receives the state before tokens 0, 64, 128, ...
  *   (states[:, 0] = init_state), which ssd_gated_scan_bwd takes.
  * Gates, decays and the carried state are fp32 for both types; y is the fp32
- * state rounded once.  A gate_x below -41.5 counts as -41.5 (i = 2^-60); a gate_a
+ * state rounded once.  A token's rounding errors are relative to what it keeps of
+ * the state, a_t |h_{t-1}|, and to its input, however small a_t is.  After an
+ * infinite state (an infinite input or carried state, an overflow) the states read
+ * infinite or NaN up to the next restart.  A gate_x below -41.5 counts as -41.5 (i = 2^-60); a gate_a
  * below -87, or below about -46 next to such a gate_x, as shut (r = 0, the token
  * changes nothing).  Results do not depend on timing (no atomics).
  * Supported: channels a multiple of 8 (bf16) or 4 (fp32), batch <= 65535,

@@ -3,12 +3,12 @@
 //
 // A step h <- a h + u is an affine map, and maps compose: (A, H) after (A', H')
 // is (A A', A H' + H).  So a sequence is cut into groups of 8 consecutive
-// tokens (4 in the fp32 forward), each thread runs its group from zero, the
-// groups' maps are composed, and each thread then replays its group from the
-// state that enters it.  The replay costs two packed operations per token on
-// values that are still in registers, while the gates (about 4
-// special-function results per element) are formed once and the inputs are
-// read once.
+// tokens (4 in the fp32 forward), each thread composes its group's maps, and the
+// groups' maps are composed in turn.  The forward keeps the maps from the group's
+// start up to each token in registers: a token's state is then one packed operation
+// on the state that enters the group.  The gradient replays its group from there.
+// The gates (about 4 special-function results per element) are formed once and the
+// inputs are read once.
 //
 // A compute warp takes one group of tokens of 64 channels (a pair per lane);
 // the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens;
@@ -140,36 +140,62 @@ __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& 
     i = mul2(inv, ea);
 }
 
-// em1 = a - 1 = e^la - 1 (la <= 0) and a.  a = 1 + em1 enters the recurrence as
-// h + em1 h, so that a decay near 1 keeps its relative accuracy in la, and
-// 1 - a^2 = -em1 (2 + em1) without cancellation.  (The step rounds at 2^-24 of the
-// state before it, also where a small decay leaves little of that; a h + u
-// for such tokens, chosen token by token, made every call 3 % slower.)
-// Down to -1/4 em1 = la + la^2 q, q the cubic that is nearest to
-// (e^la - 1 - la) / la^2 there by em1's relative error (fitted: off by 2^-28 of
-// em1; the series needs another term), beyond from e^la.  la never falls below
-// the channel's own -scale softplus(decay), so where that is above -1/4 (SLOW; the
-// usual decays of 0.9 to 0.999 at the open gate) the second form is not
-// evaluated.  The choice is made once per group, not per token: a branch between
-// the tokens kept them from overlapping (220 cycles per token and warp).
-template <bool EXACT, bool SLOW>
-__device__ __forceinline__ void decays(float2 la, float2& em1, float2& a) {
+// What a token keeps of the state, as the multiplier m of two step forms.  Down to
+// la = -1/4 (la = log a <= 0) m = a - 1 <= 0 and the step is h + m h: a decay near 1
+// keeps its relative accuracy in la, and 1 - a^2 = -m (2 + m) is formed without
+// cancellation.  Beyond, m = a > 0 and the step is m h: the little that such a
+// token keeps is not rounded at the size of the whole (h + (a - 1) h was off by 6 % of
+// a h at la = -16, and lost it at -20).  A decay below 2^-126 counts as 2^-149, so that m
+// stays positive.  m = a - 1 is la + la^2 q, q the cubic that is nearest to
+// (e^la - 1 - la) / la^2 there by m's relative error (fitted: off by 2^-28 of m; the
+// series needs another term).  la never falls below the channel's own -scale
+// softplus(decay), so where that is above -1/4 (SLOW; the usual decays of 0.9 to
+// 0.999 at the open gate) the second form is not evaluated.  The choice is made
+// once per group, not per token: a branch between the tokens kept them from
+// overlapping (220 cycles per token and warp).
+template <bool EXACT, bool SLOW> __device__ __forceinline__ float2 decays(float2 la) {
     float2 q = dup(0.0075347102f);
     q = fma2(q, la, dup(0.041502319f));
     q = fma2(q, la, dup(0.16665322f));
     q = fma2(q, la, dup(0.49999964f));
-    em1 = fma2(mul2(q, la), la, la);
-    a = add2(em1, dup(1.0f));
+    float2 m = fma2(mul2(q, la), la, la);
     if constexpr (!SLOW) {
         const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-        const bool nx = la.x >= -0.25f, ny = la.y >= -0.25f;
-        a = make_float2(nx ? a.x : e.x, ny ? a.y : e.y);
-        em1 = make_float2(nx ? em1.x : e.x - 1.0f, ny ? em1.y : e.y - 1.0f);
+        const float least = __int_as_float(1);
+        m = make_float2(la.x >= -0.25f ? m.x : max_nan(e.x, least), la.y >= -0.25f ? m.y : max_nan(e.y, least));
     }
+    return m;
+}
+// where m is a itself (SLOW: nowhere)
+struct Far {
+    bool x, y;
+};
+template <bool SLOW> __device__ __forceinline__ Far far_of(float2 m) {
+    return SLOW ? Far{false, false} : Far{m.x > 0.0f, m.y > 0.0f};
+}
+__device__ __forceinline__ float2 choose(Far far, float2 yes, float2 no) {
+    return make_float2(far.x ? yes.x : no.x, far.y ? yes.y : no.y);
+}
+// a h + u, a h and a
+__device__ __forceinline__ float2 step(Far far, float2 m, float2 h, float2 u) {
+    return add2(choose(far, dup(0.0f), h), fma2(m, h, u));
+}
+__device__ __forceinline__ float2 keep(Far far, float2 m, float2 h) { return fma2(m, h, choose(far, dup(0.0f), h)); }
+__device__ __forceinline__ float2 decay_of(Far far, float2 m) { return add2(m, choose(far, dup(0.0f), dup(1.0f))); }
+// 1 - a^2: of m = a - 1 as -m (2 + m), of m = a by one of two ways that cost alike.
+// The forward takes 1 - m m, by other constants in the same two operations (b8 L4096
+// C2048 bf16, decays from 0.3 on: 141 us, by the other way 143), the gradient goes
+// through m - 1 (214 us at the usual decays, whose own code is the same but for the
+// registers that it is left; by the other way 218).
+template <bool SLOW, bool DIRECT> __device__ __forceinline__ float2 one_less_square(Far far, float2 m) {
+    if constexpr (!SLOW && DIRECT)
+        return fma2(m, fma2(m, dup(-1.0f), choose(far, dup(0.0f), dup(-2.0f))), choose(far, dup(1.0f), dup(0.0f)));
+    if constexpr (!SLOW) m = add2(m, choose(far, dup(-1.0f), dup(0.0f)));
+    return mul2(m, fma2(m, dup(-1.0f), dup(-2.0f)));
 }
 // sqrt(1 - a^2)
-__device__ __forceinline__ float2 input_weight(float2 em1) {
-    const float2 n2 = mul2(em1, fma2(em1, dup(-1.0f), dup(-2.0f)));
+template <bool SLOW, bool DIRECT> __device__ __forceinline__ float2 input_weight(Far far, float2 m) {
+    const float2 n2 = one_less_square<SLOW, DIRECT>(far, m);
     return make_float2(sqrt_approx(n2.x), sqrt_approx(n2.y));
 }
 // -scale * softplus(decay) of a pair of channels (0 outside them)
@@ -424,33 +450,41 @@ __global__ void __launch_bounds__(kThreads, 3)
                 flag = reset_flag<TPT>(p.reset, b, t + round, L, lane);
             }
             wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
-            // the gates and the group's map
-            float2 em1[TPT], u[TPT];
+            // the gates and the maps from the group's start up to each token
+            float2 As[TPT], Hs[TPT];
             float2 A = dup(1.0f), H = dup(0.0f);
             by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
+                constexpr bool SLOW = decltype(is_slow)::value;
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
                     const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    float2 r, i, a, ga = read_gates(*at(2, j), kLeastA);
+                    float2 r, i, ga = read_gates(*at(2, j), kLeastA);
                     if (rs) ga = dup(0.0f);  // not used: whatever it holds
                     sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r, i);
-                    decays<EXACT, decltype(is_slow)::value>(mul2(k, r), em1[j], a);
-                    float2 n = input_weight(em1[j]);
+                    As[j] = decays<EXACT, SLOW>(mul2(k, r));  // (the token's multiplier, then its map)
+                    float2 n = input_weight<SLOW, true>(far_of<SLOW>(As[j]), As[j]);
                     if (rs) n = dup(1.0f);
-                    u[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
-                }
-                if (t + TPT > L) {  // tokens past the end change nothing
-#pragma unroll
-                    for (int j = 0; j < TPT; ++j)
-                        if (t + j >= L) em1[j] = u[j] = dup(0.0f);
+                    Hs[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
                 }
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
                     const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    A = rs ? dup(0.0f) : fma2(em1[j], A, A);
-                    H = rs ? u[j] : add2(H, fma2(em1[j], H, u[j]));
+                    const Far far = far_of<SLOW>(As[j]);
+                    H = rs ? Hs[j] : step(far, As[j], H, Hs[j]);
+                    A = rs ? dup(0.0f) : keep(far, As[j], A);
+                    As[j] = A;
+                    Hs[j] = H;
                 }
             });
+            if (t + TPT > L) {  // the group's map is its last token's
+                A = dup(1.0f);
+                H = dup(0.0f);
+#pragma unroll
+                for (int j = 0; j < TPT; ++j) {
+                    A = t + j < L ? As[j] : A;
+                    H = t + j < L ? Hs[j] : H;
+                }
+            }
             ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
             if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
             __syncwarp();
@@ -458,17 +492,19 @@ __global__ void __launch_bounds__(kThreads, 3)
             // the outputs, over gate_a's tile; the ninth warp's wait on its cluster is
             // bounded and it always arrives
             wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
-            float2 h = ex.entering[warp][lane];
+            const float2 h = ex.entering[warp][lane];
             // (a kept state's token starts a group)
             if (p.states && active && t < L && t % kInterval == 0)
                 *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
-            by_group<RESET>(true, rst, [&](auto, auto restarts) {
+            if (RESET && rst != 0) {
+                const int from = __ffs(static_cast<int>(rst)) - 1;  // where h is dropped
 #pragma unroll
-                for (int j = 0; j < TPT; ++j) {
-                    h = decltype(restarts)::value && ((rst >> j) & 1) ? u[j] : add2(h, fma2(em1[j], h, u[j]));
-                    *at(2, j) = Pair<T>::narrow(h);
-                }
-            });
+                for (int j = 0; j < TPT; ++j)
+                    *at(2, j) = Pair<T>::narrow(j >= from ? Hs[j] : fma2(As[j], h, Hs[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < TPT; ++j) *at(2, j) = Pair<T>::narrow(fma2(As[j], h, Hs[j]));
+            }
             tc::fence_smem_async();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
@@ -496,7 +532,8 @@ struct ExchangeBwd {
     int abort;
 };
 
-// A state is parked in the places of its token's gates, which are read by then.
+// The places of a token's gates, once they are read, hold its u and then the state
+// before it.
 __device__ __forceinline__ void park(uint32_t* gx, uint32_t* ga, float2 h) {
     *gx = __float_as_uint(h.x);
     *ga = __float_as_uint(h.y);
@@ -638,27 +675,30 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             const int left = t + TPT <= L ? TPT : static_cast<int>(L - t < 0 ? 0 : L - t);
             wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
-            float2 r[TPT], i[TPT], em1[TPT];
+            float2 r[TPT], i[TPT], m[TPT];
             float2 A = dup(1.0f), H = dup(0.0f), G = dup(0.0f);
             by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
+                constexpr bool SLOW = decltype(is_slow)::value;
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
                     const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    float2 a, ga = read_gates(*at(2, j), kLeastA);
+                    float2 ga = read_gates(*at(2, j), kLeastA);
                     if (rs) ga = dup(0.0f);
                     sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r[j], i[j]);
-                    decays<EXACT, decltype(is_slow)::value>(mul2(k, r[j]), em1[j], a);
-                    float2 n = input_weight(em1[j]);
+                    m[j] = decays<EXACT, SLOW>(mul2(k, r[j]));
+                    float2 n = input_weight<SLOW, false>(far_of<SLOW>(m[j]), m[j]);
                     if (rs) n = dup(1.0f);
                     float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                    if (j >= left) em1[j] = u = dup(0.0f);  // tokens past the end change nothing
-                    A = rs ? dup(0.0f) : fma2(em1[j], A, A);
-                    H = rs ? u : add2(H, fma2(em1[j], H, u));
+                    if (j >= left) m[j] = u = dup(0.0f);  // tokens past the end change nothing
+                    park(at(1, j), at(2, j), u);
+                    const Far far = far_of<SLOW>(m[j]);
+                    A = rs ? dup(0.0f) : keep(far, m[j], A);
+                    H = rs ? u : step(far, m[j], H, u);
                 }
 #pragma unroll
                 for (int j = TPT - 1; j >= 0; --j) {  // (dy reads as zero past the end)
                     G = add2(G, Pair<T>::widen(*at(3, j)));
-                    G = decltype(restarts)::value && ((rst >> j) & 1) ? dup(0.0f) : fma2(em1[j], G, G);
+                    G = decltype(restarts)::value && ((rst >> j) & 1) ? dup(0.0f) : keep(far_of<SLOW>(m[j]), m[j], G);
                 }
             });
             ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
@@ -669,21 +709,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
             const float4 in = ex.entering[warp][lane];
             float2 h = make_float2(in.x, in.y), g = make_float2(in.z, in.w);
-            // What follows is formed again from r, i and em1: kept over the wait, n and u
-            // of the group would cost 32 more registers.
+            // What follows is formed again from r, i and m: kept over the wait, n of the
+            // group would cost 16 more registers.
 #pragma unroll
             for (int j = 0; j < TPT; ++j)
                 asm volatile(""
-                             : "+f"(em1[j].x), "+f"(em1[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
+                             : "+f"(m[j].x), "+f"(m[j].y), "+f"(r[j].x), "+f"(r[j].y), "+f"(i[j].x), "+f"(i[j].y));
             by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
+                constexpr bool SLOW = decltype(is_slow)::value;
                 // forwards: the state before each token
 #pragma unroll
                 for (int j = 0; j < TPT; ++j) {
+                    const float2 u = unpark(at(1, j), at(2, j));
                     park(at(1, j), at(2, j), h);
                     const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    const float2 n = rs ? dup(1.0f) : input_weight(em1[j]);
-                    const float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                    h = rs ? u : add2(h, fma2(em1[j], h, u));
+                    h = rs ? u : step(far_of<SLOW>(m[j]), m[j], h, u);
                 }
                 // backwards: the outputs
 #pragma unroll
@@ -692,14 +732,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float2 x = Pair<T>::widen(*at(0, j)), hp = unpark(at(1, j), at(2, j));
                     g = add2(g, Pair<T>::widen(*at(3, j)));
                     const float2 ix = mul2(i[j], x), la = mul2(k, r[j]);
-                    float2 a = add2(em1[j], dup(1.0f));
-                    if constexpr (!decltype(is_slow)::value) {  // a small decay as it is, not as 1 + em1
-                        const float2 e = exp2_scaled<EXACT>(la, kLog2eHi, kLog2eLo);
-                        a = make_float2(la.x >= -0.25f ? a.x : e.x, la.y >= -0.25f ? a.y : e.y);
-                    }
+                    const Far far = far_of<SLOW>(m[j]);
+                    const float2 a = decay_of(far, m[j]);
                     // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
                     // gives a finite dla, times la = 0
-                    const float2 n2 = mul2(em1[j], fma2(em1[j], dup(-1.0f), dup(-2.0f)));
+                    const float2 n2 = one_less_square<SLOW, false>(far, m[j]);
                     const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)),
                                                   rsqrt_approx(max_nan(n2.y, 1e-36f)));
                     const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
@@ -709,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (rs) dla = dup(0.0f);
                     const float2 dga = mul2(dla, fma2(la, mul2(r[j], dup(-1.0f)), la));
                     if (j < left) sum = fma2(dla, r[j], sum);
-                    g = rs ? dup(0.0f) : fma2(em1[j], g, g);
+                    g = rs ? dup(0.0f) : keep(far, m[j], g);
                     *at(0, j) = Pair<T>::narrow(dx);
                     *at(1, j) = Pair<T>::narrow(dgx);
                     *at(2, j) = Pair<T>::narrow(dga);
@@ -808,13 +845,14 @@ __global__ void __launch_bounds__(kUpdateThreads) gated_update_kernel(GatedUpdat
         float2 h[2] = {make_float2(st[r].x, st[r].y), make_float2(st[r].z, st[r].w)};
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            float2 rg, ig, em1, a;
+            float2 rg, ig;
             if (rs[r]) av[j] = dup(0.0f);
             sigmas<EXACT>(least_gates<EXACT>(av[j], -87.0f), least_gates<EXACT>(iv[j], -41.5f), rg, ig);
-            decays<EXACT, false>(mul2(k[j], rg), em1, a);
-            if (rs[r]) em1 = dup(-1.0f);
-            const float2 u = mul2(mul2(input_weight(em1), ig), xv[j]);
-            h[j] = rs[r] ? u : add2(h[j], fma2(em1, h[j], u));
+            const float2 la = mul2(k[j], rg), m = decays<EXACT, false>(la);
+            const Far far{!(la.x >= -0.25f), !(la.y >= -0.25f)};  // (the choice that decays makes)
+            const float2 n = rs[r] ? dup(1.0f) : input_weight<false, true>(far, m);
+            const float2 u = mul2(mul2(n, ig), xv[j]);
+            h[j] = rs[r] ? u : step(far, m, h[j], u);
         }
         const int64_t i = (row0 + r) * quads + quad;
         reinterpret_cast<float4*>(p.new_state)[i] = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);

@@ -48,6 +48,13 @@ def gates(gate_a, gate_x, decay, scale, reset):
     return r, i, la, a, em1, n
 
 
+def kept(la, a, em1, h):
+    """Error of a h: with a decay near 1 as h + em1 h, em1 off by D of itself, beyond as
+    e^la h, la off by D of itself; the old state is never rounded at its own size
+    where little of it is kept."""
+    return np.where(la >= -0.25, np.abs(em1) * D, a * (1.0 + np.abs(la)) * D + TINY) * np.abs(h)
+
+
 def gated_scan(x, gate_a, gate_x, decay, init=None, reset=None, scale=8.0):
     """[b, L, C] arrays -> dict of y, final, states and their error bounds e_*."""
     x, gate_a, gate_x, decay = map(_np, (x, gate_a, gate_x, decay))
@@ -68,9 +75,8 @@ def gated_scan(x, gate_a, gate_x, decay, init=None, reset=None, scale=8.0):
         if reset is not None:
             keep = keep & (reset[:, t] == 0)[:, None]
         hn = np.where(keep, a * np.where(keep, h, 0.0), 0.0) + u[:, t]
-        # h + em1 h: em1's own error and a rounding at the old state's size, however
-        # small a is; then four roundings of the new state
-        err = np.where(keep, a * err + np.abs(em1[:, t] * np.where(keep, h, 0.0)) * D, 0.0) \
+        # what is kept of the old state, then four roundings of the new one
+        err = np.where(keep, a * err + kept(la[:, t], a, em1[:, t], np.where(keep, h, 0.0)), 0.0) \
             + np.abs(u[:, t]) * D + 4 * U * np.abs(hn)
         h = hn
         y[:, t], e_y[:, t] = h, err
@@ -122,7 +128,7 @@ def gated_scan_bwd(x, gate_a, gate_x, decay, dy, init=None, reset=None, d_final=
         e_sums += (e_dla * r[:, t] + D * np.abs(dla * r[:, t])).sum(0)
         mags += np.abs(dla * r[:, t]).sum(0)
         c2 = np.where(on, a * np.where(on, g, 0.0), 0.0)
-        e_carry = np.where(on, a * e_g + np.abs(em1[:, t] * g) * D + 4 * U * np.abs(c2), 0.0)
+        e_carry = np.where(on, a * e_g + kept(la[:, t], a, em1[:, t], g) + 4 * U * np.abs(c2), 0.0)
         carry = c2
     ks = -scale * sigma(decay)
     o["ddecay"] = ks * sums

@@ -1,0 +1,65 @@
+"""The gated linear recurrence where it could go wrong: states that are large beside
+what a token keeps of them, and states that are not finite."""
+import pytest
+import torch
+
+import mamba_ssd_scan_b200 as ssd
+from oracle import mixers as om
+from test_gpu_mixers import dev, within
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def wide_inputs(b, L, C, dtype, seed, resets=0):
+    """Decays from 1 down to e^-48, inputs and incoming gradients of sizes from 1e-3 to
+    1e6 behind gates from open to nearly shut (e^-10: their own rounding stays
+    within the definition's bound), a carried state and a final gradient of 1e4 to
+    1e8."""
+    g = torch.Generator().manual_seed(seed)
+    rn = lambda *s: torch.randn(s, generator=g)
+    sized = lambda lo, hi, *s: rn(*s) * 10 ** (lo + (hi - lo) * torch.rand(s, generator=g))
+    d = {"x": sized(-3, 6, b, L, C).to(dtype), "gate_a": (1 + rn(b, L, C)).clamp(-3, 4).to(dtype),
+         "gate_x": (14 * torch.rand((b, L, C), generator=g) - 10).to(dtype),
+         "decay": torch.linspace(-6, 6, C)[torch.randperm(C, generator=g)],
+         "init_state": sized(4, 8, b, C), "reset": None}
+    if resets:
+        d["reset"] = (torch.rand((b, L), generator=g) < resets / L).to(torch.uint8)
+    return d, sized(-3, 6, b, L, C).to(dtype), sized(4, 8, b, C)
+
+
+def check_scan(d, dy, df, what=""):
+    g = dev(d)
+    y, fin, st = ssd.ssd_gated_scan(**g, return_final_state=True, return_states=True)
+    ref = om.gated_scan(d["x"], d["gate_a"], d["gate_x"], d["decay"], d["init_state"], d["reset"])
+    within(y, ref["y"], ref["e_y"], what + "y")
+    within(fin, ref["final"], ref["e_final"], what + "final_state")
+    within(st, ref["states"], ref["e_states"], what + "states")
+    g.pop("init_state")
+    o = ssd.ssd_gated_scan_bwd(dy=dy.to(DEV), states=st, d_final=df.to(DEV), **g)
+    ref = om.gated_scan_bwd(d["x"], d["gate_a"], d["gate_x"], d["decay"], dy, d["init_state"], d["reset"], df)
+    for k in ("dx", "dgate_a", "dgate_x", "ddecay", "d_init"):
+        within(o[k], ref[k], ref["e_" + k], what + k)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("b,L,C,resets", [(2, 1, 72, 0), (3, 9, 64, 0), (1, 70, 200, 4), (1, 1500, 72, 0),
+                                          (2, 1301, 136, 40)])
+def test_small_decays_keep_what_is_left(dtype, b, L, C, resets):
+    """A token that keeps little of a large state keeps that little accurately: the
+    definition's bound counts a |h|, not |h|."""
+    check_scan(*wide_inputs(b, L, C, dtype, seed=L, resets=resets))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_decode_steps_at_small_decays(dtype):
+    d, _, _ = wide_inputs(600, 12, 72, dtype, seed=4)
+    g = dev(d)
+    ref = om.gated_scan(d["x"], d["gate_a"], d["gate_x"], d["decay"], d["init_state"])
+    st = g["init_state"].clone()
+    for t in range(12):
+        y = ssd.ssd_gated_state_update(st, *(g[k][:, t].contiguous() for k in ("x", "gate_a", "gate_x")), g["decay"])
+        within(y, ref["y"][:, t], ref["e_y"][:, t], f"y of step {t}")
+    within(st, ref["final"], ref["e_final"], "state")
