@@ -182,6 +182,9 @@ __device__ __forceinline__ float2 step(Far far, float2 m, float2 h, float2 u) {
 }
 __device__ __forceinline__ float2 keep(Far far, float2 m, float2 h) { return fma2(m, h, choose(far, dup(0.0f), h)); }
 __device__ __forceinline__ float2 decay_of(Far far, float2 m) { return add2(m, choose(far, dup(0.0f), dup(1.0f))); }
+// A multiplier that changes no state and no adjoint, infinite ones included: a = 1, or
+// a - 1 = 2^-149, which adds nothing to a finite h (0 would be 0 times infinity).
+template <bool SLOW> constexpr float kNothing = SLOW ? 1.401298464e-45f : 1.0f;
 // 1 - a^2: of m = a - 1 as -m (2 + m), of m = a by one of two ways that cost alike.
 // The forward takes 1 - m m, by other constants in the same two operations (b8 L4096
 // C2048 bf16, decays from 0.3 on: 141 us, by the other way 143), the gradient goes
@@ -689,7 +692,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float2 n = input_weight<SLOW, false>(far_of<SLOW>(m[j]), m[j]);
                     if (rs) n = dup(1.0f);
                     float2 u = mul2(n, mul2(i[j], Pair<T>::widen(*at(0, j))));
-                    if (j >= left) m[j] = u = dup(0.0f);  // tokens past the end change nothing
+                    if (j >= left) {  // tokens past the end change nothing
+                        m[j] = dup(kNothing<SLOW>);
+                        u = dup(0.0f);
+                    }
                     park(at(1, j), at(2, j), u);
                     const Far far = far_of<SLOW>(m[j]);
                     A = rs ? dup(0.0f) : keep(far, m[j], A);

@@ -63,3 +63,27 @@ def test_decode_steps_at_small_decays(dtype):
         y = ssd.ssd_gated_state_update(st, *(g[k][:, t].contiguous() for k in ("x", "gate_a", "gate_x")), g["decay"])
         within(y, ref["y"][:, t], ref["e_y"][:, t], f"y of step {t}")
     within(st, ref["final"], ref["e_final"], "state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("decay", [-6.0, 3.0])
+def test_an_infinite_end_is_the_final_state(dtype, decay):
+    """The final state is the last token's, infinite or not, and an infinite d_final
+    enters at the last token, wherever the sequence ends in its group of tokens."""
+    g = torch.Generator().manual_seed(0)
+    C = 8
+    for L in list(range(1, 18)) + [63, 64, 65, 500, 1029]:
+        x, ga, gx, dy = (torch.randn((1, L, C), generator=g).to(dtype).to(DEV) for _ in range(4))
+        x[0, L - 1, 2], x[0, L - 1, 5] = float("inf"), float("-inf")
+        dec = torch.full((C,), decay, device=DEV)
+        y, fin, st = ssd.ssd_gated_scan(x, ga, gx, dec, return_final_state=True, return_states=True)
+        assert y[0, L - 1, 2] == float("inf") and y[0, L - 1, 5] == float("-inf")
+        assert fin[0, 2] == float("inf") and fin[0, 5] == float("-inf"), L
+        assert torch.isfinite(fin[0, [0, 1, 3, 4, 6, 7]]).all(), L
+        x[0, L - 1, 2], x[0, L - 1, 5] = 1.0, 1.0
+        df = torch.zeros((1, C), device=DEV)
+        df[0, 3] = float("inf")
+        o = ssd.ssd_gated_scan_bwd(x, ga, gx, dec, dy, st, d_final=df)
+        # dx = g n i, g infinite
+        assert torch.isinf(o["dx"][0, L - 1, 3]) and o["dx"][0, L - 1, 3] > 0, L
+        assert torch.isfinite(o["dx"][0, :, [0, 1, 4, 6, 7]]).all(), L
