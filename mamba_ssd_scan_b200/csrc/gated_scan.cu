@@ -209,7 +209,9 @@ __device__ __forceinline__ float2 decay_rates(const GatedScanParams& p, int64_t 
 __device__ __forceinline__ float sigma_f32(float v) { return 1.0f / (1.0f + expf(-v)); }
 
 // ---- clusters ----
+// (the barrier is an aligned one: a warp that parted before it joins first)
 __device__ __forceinline__ void cluster_sync_all() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // the shared::cluster address of this CTA's shared variable in CTA `rank`
