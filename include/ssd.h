@@ -618,8 +618,10 @@ ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* args, void*
  *   f = position * inv_freq[j],  j < rot_dim / 2
  * for the pairs (a, b) = (j, j + rot_dim / 2), or (2j, 2j + 1) with `adjacent`;
  * elements from rot_dim on are not rotated.  The turns per position, inv_freq /
- * (2 pi), are formed in fp64 and held as a 64-bit fraction, so that whole turns
- * drop out of the product with the position exactly; cosine and sine are fp32.
+ * (2 pi), are formed in two fp64 parts and held as a 64-bit fraction, so that whole
+ * turns drop out of the product with the position exactly: the angle is off by less
+ * than 2^-25 of a turn at positions up to 2^31, whatever inv_freq; cosine and sine
+ * are fp32.
  * Layouts: q, q_out: batch * seqlen tokens q_stride / q_out_stride elements
  *   apart, each with q_heads dense heads of headdim elements, dtype; k, k_out
  *   alike (NULL with k_heads = 0).  So slices of one packed row per token are

@@ -78,9 +78,10 @@ __device__ __forceinline__ float2 cos_sin_turn(float f) {
 // lanes read them: a slot's N pairs are N / 2 16-byte chunks (c0, c1, s0, s1),
 // chunk k of slot l of token t at ((t * N / 2) + k) * rs + l.  A thread keeps one
 // pair j and steps through the tokens.  Its turns per position, inv_freq /
-// (2 pi), are held as a 64-bit fraction of a turn (formed in fp64), so the angle
-// is an integer product that drops the whole turns by itself: off by less than
-// 2^-25 of a turn at positions up to 2^31.
+// (2 pi), are held as a 64-bit fraction of a turn (formed in two fp64 parts, so that
+// it is right to 2^-63 at any frequency), so the angle is an integer product that
+// drops the whole turns by itself: off by less than 2^-25 of a turn at positions up
+// to 2^31.
 template <int N> struct Angles {
     int t0, tstep, place;  // first token, tokens per step (0: no pair), float offset of the pair in a token's chunks
     int64_t turn;          // the fraction of a turn per position, times 2^64
@@ -96,8 +97,12 @@ template <int N> struct Angles {
             tstep = 0;
             return;
         }
-        const double f = static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577;  // 1 / (2 pi)
-        turn = static_cast<int64_t>((f - rint(f)) * 18446744073709549568.0);  // just below 2^64: no overflow at 1/2
+        // inv_freq / (2 pi) as f + e, 1 / (2 pi) in two parts; whole turns come off f and e
+        // exactly (a fraction of 1/2 is cut off at 2^63 - 1)
+        constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18;
+        const double v = static_cast<double>(p.inv_freq[j]), f = v * kHi, e = fma(v, kLo, fma(v, kHi, -f));
+        turn = static_cast<int64_t>(static_cast<uint64_t>(__double2ll_rn((f - rint(f)) * 18446744073709551616.0)) +
+                                    static_cast<uint64_t>(__double2ll_rn((e - rint(e)) * 18446744073709551616.0)));
         int l, w;  // the slot that holds pair j and its place there
         if (!p.adjacent) {
             l = j / N;
