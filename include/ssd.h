@@ -437,7 +437,8 @@ ssd_status ssd_causal_conv1d(const ssd_conv1d_args* args, void* stream);
 
 /* Synchronises `stream` and returns SSD_ERR_TIMEOUT if a ssd_causal_conv1d or
  * ssd_causal_conv1d_bwd launch on this device timed out on an internal wait
- * since the last check (the flag is cleared), else SSD_OK. */
+ * since the last check, else SSD_OK.  A launch on another stream that times out
+ * meanwhile is reported by this check or the next. */
 ssd_status ssd_conv1d_check_status(void* stream);
 
 /* Gradients of ssd_causal_conv1d: of J = sum dy . y + d_final : final_state
@@ -545,7 +546,8 @@ ssd_status ssd_gated_scan(const ssd_gated_scan_args* args, void* stream);
 
 /* Synchronises `stream` and returns SSD_ERR_TIMEOUT if a ssd_gated_scan or
  * ssd_gated_scan_bwd launch on this device gave up on an internal wait since
- * the last check (its outputs are invalid; the flag is cleared), else SSD_OK. */
+ * the last check (its outputs are invalid), else SSD_OK.  A launch on another stream
+ * that gives up meanwhile is reported by this check or the next. */
 ssd_status ssd_gated_scan_check_status(void* stream);
 
 /* Gradients of ssd_gated_scan: of J = sum dy . y + d_final . h_L with respect to

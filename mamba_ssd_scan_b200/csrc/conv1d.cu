@@ -30,9 +30,8 @@ constexpr int MAXROWB = 2048;  // bytes of one tile row (the CTA's channel block
 constexpr int CPT = 4;         // channels per consumer thread
 template <typename T> constexpr int kMaxConsumers = MAXROWB / (CPT * static_cast<int>(sizeof(T)));
 
-// SSD_ERR_TIMEOUT once a forward launch gave up on a wait; read and cleared
-// by ssd_conv1d_check_status.
-__device__ int g_conv_status;
+// Forward CTAs that gave up on a wait (ssd_conv1d_check_status).
+__device__ uint32_t g_conv_gave_up;
 
 // Four consecutive channels of one token, widened to fp32 pairs.
 template <typename T> struct Quad;
@@ -259,7 +258,7 @@ __global__ void __launch_bounds__(kMaxConsumers<T> + 32)
         // before the CTA's shared memory goes away, and report it.
         for (int jj = issued - NSTAGE < 0 ? 0 : issued - NSTAGE; jj < issued; ++jj)
             mbar_wait(smem_u32(&full[jj % NSTAGE]), (jj / NSTAGE) & 1);
-        atomicExch(&g_conv_status, static_cast<int>(SSD_ERR_TIMEOUT));
+        atomicAdd(&g_conv_gave_up, 1u);
     }
 }
 
@@ -399,13 +398,8 @@ template cudaError_t launch_conv1d<float>(const ConvParams&, bool, cudaStream_t)
 template cudaError_t launch_conv1d<__nv_bfloat16>(const ConvParams&, bool, cudaStream_t);
 
 cudaError_t conv1d_take_status(int* v, cudaStream_t s) {
-    int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_conv_status, sizeof(int), 0,
-                                              cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess)
-        e = cudaMemcpyToSymbolAsync(g_conv_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return e;
+    static GaveUp gave_up;
+    return gave_up.take(g_conv_gave_up, v, s);
 }
 
 }  // namespace ssd

@@ -44,9 +44,8 @@ constexpr int kRing = 3;  // batches in shared memory
 template <typename T> constexpr int kRowBytes = CPW * sizeof(T);
 template <typename T> constexpr int kWarpBytes = kRing * 2 * kBatch<T> * kRowBytes<T>;  // x and dy tiles
 
-// SSD_ERR_TIMEOUT once a launch gave up on a wait; read and cleared by
-// ssd_conv1d_check_status.
-__device__ int g_conv_bwd_status;
+// Lanes that gave up on a wait (ssd_conv1d_check_status).
+__device__ uint32_t g_conv_bwd_gave_up;
 
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
@@ -229,7 +228,7 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
 #pragma unroll
         for (int k = 0; k <= K; ++k) *reinterpret_cast<float2*>(row + k * Cn) = k < K ? dw[k < K ? k : 0] : db;
     }
-    if (!ok) atomicExch(&g_conv_bwd_status, static_cast<int>(SSD_ERR_TIMEOUT));
+    if (!ok) atomicAdd(&g_conv_bwd_gave_up, 1u);
 }
 
 constexpr int kSumWarps = 8;
@@ -318,12 +317,8 @@ template cudaError_t launch_conv1d_bwd<float>(const ConvBwdParams&, cudaStream_t
 template cudaError_t launch_conv1d_bwd<__nv_bfloat16>(const ConvBwdParams&, cudaStream_t);
 
 cudaError_t conv1d_bwd_take_status(int* v, cudaStream_t s) {
-    int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_conv_bwd_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess)
-        e = cudaMemcpyToSymbolAsync(g_conv_bwd_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return e;
+    static GaveUp gave_up;
+    return gave_up.take(g_conv_bwd_gave_up, v, s);
 }
 
 }  // namespace ssd

@@ -255,9 +255,8 @@ __device__ __forceinline__ bool wait_phase(uint32_t mbar, uint32_t parity, uint3
     return false;
 }
 
-// SSD_ERR_TIMEOUT once a scan or its gradient gave up on a wait; read and
-// cleared by ssd_gated_scan_check_status.
-__device__ int g_gated_status;
+// CTAs of the scan and its gradient that gave up on a wait (ssd_gated_scan_check_status).
+__device__ uint32_t g_gated_gave_up;
 
 // restarts among the group's tokens: lane j's flag of token t0 + j
 template <int N>
@@ -517,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     __syncthreads();
     if (cl > 1) cluster_sync_all();  // no peer's map arrives after a CTA has left
-    if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
+    if (threadIdx.x == 0 && ex.abort) atomicAdd(&g_gated_gave_up, 1u);
 }
 
 // The gradient, the same way from the last token to the first: a group also has
@@ -778,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         *reinterpret_cast<float2*>(p.partial + (b * cl + rank) * C + c) = s;
     }
     if (cl > 1) cluster_sync_all();
-    if (threadIdx.x == 0 && ex.abort) atomicExch(&g_gated_status, static_cast<int>(SSD_ERR_TIMEOUT));
+    if (threadIdx.x == 0 && ex.abort) atomicAdd(&g_gated_gave_up, 1u);
 }
 
 // ddecay = -scale * sigma(decay) * the sum of dla * r over batch and time
@@ -1003,12 +1002,8 @@ template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p
 }
 
 cudaError_t gated_scan_take_status(int* v, cudaStream_t s) {
-    int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbolAsync(v, g_gated_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess)
-        e = cudaMemcpyToSymbolAsync(g_gated_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    return e;
+    static GaveUp gave_up;
+    return gave_up.take(g_gated_gave_up, v, s);
 }
 
 template cudaError_t launch_gated_scan<float>(const GatedScanParams&, cudaStream_t);

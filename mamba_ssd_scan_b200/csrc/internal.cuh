@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/ssd.h"
 
 namespace ssd {
@@ -135,6 +137,30 @@ __device__ __forceinline__ float softplus_f32(float u) {
     return fmaxf(u, 0.0f) + log1pf(expf(-fabsf(u)));
 }
 
+// Waits that gave up.  A kernel adds to its own __device__ word (one per device), and
+// nothing clears that: a check copies the word and compares it with what the checks
+// before it had seen, so that a call on another stream that gives up meanwhile is
+// reported by this check or the next.
+struct GaveUp {
+    static constexpr int kDevices = 64;
+    std::atomic<uint32_t> seen[kDevices] = {};
+    // *v = SSD_ERR_TIMEOUT if the word on the current device counts waits that no check
+    // has reported, else 0 (synchronises s).
+    cudaError_t take(const uint32_t& word, int* v, cudaStream_t s) {
+        *v = 0;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && dev >= kDevices) e = cudaErrorInvalidDevice;
+        if (e != cudaSuccess) return e;
+        uint32_t now = 0, before = seen[dev].load();
+        e = cudaMemcpyFromSymbolAsync(&now, word, sizeof(now), 0, cudaMemcpyDeviceToHost, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        while (e == cudaSuccess && *v == 0 && static_cast<int32_t>(now - before) > 0)
+            if (seen[dev].compare_exchange_weak(before, now)) *v = static_cast<int>(SSD_ERR_TIMEOUT);
+        return e;
+    }
+};
+
 // Programmatic dependent launch.  A kernel launched with pdl set may start
 // while the previous kernel of the stream is still running; it must call
 // grid_dep_wait() before it reads or writes anything that kernel (or an
@@ -246,7 +272,7 @@ bool bwd_tc_supported(const FwdParams& p);
 cudaError_t launch_bwd_tc(const BwdParams& p, cudaStream_t s);
 // Shared memory (bytes) the backward's per-chunk kernels need for a shape.
 size_t bwd_smem_bytes(int64_t headdim, int64_t dstate, int64_t chunk);
-// Copies the forward kernel's device status word to *v and clears it (synchronises s).
+// *v = SSD_ERR_TIMEOUT if the forward gave up on a wait since the last check (synchronises s).
 cudaError_t conv1d_take_status(int* v, cudaStream_t s);
 
 // Tensor-core (tcgen05) variants for bf16 inputs, with their shape ranges.

@@ -62,7 +62,7 @@ struct GatedUpdateParams {
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s);
 template <typename T> cudaError_t launch_gated_scan_bwd(const GatedScanParams& p, cudaStream_t s);
 template <typename T> cudaError_t launch_gated_update(const GatedUpdateParams& p, cudaStream_t s);
-// Copies the scan's device status word to *v and clears it (synchronises s).
+// *v = SSD_ERR_TIMEOUT if the scan or its gradient gave up on a wait since the last check (synchronises s).
 cudaError_t gated_scan_take_status(int* v, cudaStream_t s);
 // Bytes of the backward's partial sums.
 size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels);
@@ -109,7 +109,7 @@ struct ConvBwdParams {
 };
 template <typename T> cudaError_t launch_conv1d_bwd(const ConvBwdParams& p, cudaStream_t s);
 size_t conv1d_bwd_partial_bytes(int64_t batch, int64_t seqlen, int64_t channels, int64_t width);
-// Copies the gradient's device status word to *v and clears it (synchronises s).
+// *v = SSD_ERR_TIMEOUT if the gradient gave up on a wait since the last check (synchronises s).
 cudaError_t conv1d_bwd_take_status(int* v, cudaStream_t s);
 
 }  // namespace ssd
