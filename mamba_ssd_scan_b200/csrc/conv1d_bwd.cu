@@ -44,7 +44,7 @@ constexpr int kRing = 3;  // batches in shared memory
 template <typename T> constexpr int kRowBytes = CPW * sizeof(T);
 template <typename T> constexpr int kWarpBytes = kRing * 2 * kBatch<T> * kRowBytes<T>;  // x and dy tiles
 
-// Lanes that gave up on a wait (ssd_conv1d_check_status).
+// Warps that gave up on a wait (ssd_conv1d_check_status).
 __device__ uint32_t g_conv_bwd_gave_up;
 
 __device__ __forceinline__ float2 dup(float v) { return make_float2(v, v); }
@@ -70,14 +70,25 @@ __device__ __forceinline__ float2 dsilu2(float2 o) {
     return mul2(sg, fma2(o, fma2(sg, dup(-1.0f), dup(1.0f)), dup(1.0f)));
 }
 
+// Bounded wait on a batch: a probe suspends the warp until the copies have landed or 2
+// us have passed, and after about a second it gives up.
+__device__ __forceinline__ bool wait_loaded(uint32_t mbar, uint32_t parity) {
+    for (uint32_t i = 0; i < 1u << 19; ++i)
+        if (tc::mbar_try_wait_hint(mbar, parity, 2000)) return true;
+    return false;
+}
+
 struct ConvBwdMaps {
     CUtensorMap x, dy, dx;
 };
 
-// segments of seg tokens (a multiple of kSegUnit), nseg per (batch, channel block)
+// segments of seg tokens (a multiple of kSegUnit), nseg per (batch, channel block).
+// `withhold` >= 0 makes the first warp leave that batch out (a test of the bounded
+// wait); -1 in normal use.
 template <typename T, int K, bool ACT>
 __global__ void __launch_bounds__(NW * 32, kPerSm)
-    conv1d_bwd_kernel(ConvBwdParams p, const __grid_constant__ ConvBwdMaps maps, int64_t seg, int nseg, int64_t warps) {
+    conv1d_bwd_kernel(ConvBwdParams p, const __grid_constant__ ConvBwdMaps maps, int64_t seg, int nseg, int64_t warps,
+                      int withhold) {
     using P = Pair<T>;
     using Raw = typename P::Raw;
     constexpr int R = kRing, KM = K - 1, TB = kBatch<T>;
@@ -103,7 +114,9 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
     const int total = nb + (K > 1 ? 1 : 0);
 
     uint8_t* ring = smem + warp * kWarpBytes<T>;
+    const int skipped = wi == 0 ? withhold : -1;
     auto load = [&](int n) {
+        if (n == skipped) return;
         const uint32_t dst = tc::smem_u32(ring) + (n % R) * 2 * kTile, bar = tc::smem_u32(&loaded[warp][n % R]);
         const int t = static_cast<int>(ta + static_cast<int64_t>(n) * TB);
         tc::mbar_expect_tx(bar, 2 * kTile);
@@ -159,12 +172,15 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         for (int k = 1; k < K; ++k) g = fma2(w[k], dv[KM + j - k], g);
         return g;
     };
-    bool ok = true;
+    int late = total;  // the batch whose wait gave up
     for (int n = 0; n < total; ++n) {
         uint8_t* tile = ring + (n % R) * 2 * kTile + lane * sizeof(Raw);
         const int64_t t0 = ta + static_cast<int64_t>(n) * TB;
         const bool halo = n == nb;
-        ok &= tc::mbar_wait(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
+        if (!__all_sync(0xffffffffu, wait_loaded(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1))) {
+            late = n;
+            break;
+        }
         const bool whole = n > 0 && !halo && t0 + TB <= L;  // inside the segment, without a condition
 #pragma unroll 1
         for (int o = 0; o < (halo ? SB : TB); o += SB, tile += SB * kRowBytes<T>) {
@@ -223,12 +239,19 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         }
     }
     if (lane == 0) tc::bulk_wait_all();
+    if (late < total) {
+        // the copies in flight land (bounded) before the warp leaves its shared memory
+        const int issued = late > 0 ? late - 1 + R : R;
+        for (int n = late; n < issued && n < total; ++n)
+            if (n != skipped) wait_loaded(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
+        if (lane == 0) atomicAdd(&g_conv_bwd_gave_up, 1u);
+        return;
+    }
     if (active) {  // row [K + 1][Cn], dbias last
         float* row = p.partial + (b * nseg + s) * (K + 1) * Cn + c;
 #pragma unroll
         for (int k = 0; k <= K; ++k) *reinterpret_cast<float2*>(row + k * Cn) = k < K ? dw[k < K ? k : 0] : db;
     }
-    if (!ok) atomicAdd(&g_conv_bwd_gave_up, 1u);
 }
 
 constexpr int kSumWarps = 8;
@@ -273,7 +296,8 @@ cudaError_t launch_act(const ConvBwdParams& p, const ConvBwdMaps& m, const ConvG
     if (e != cudaSuccess) return e;
     const auto ctas = static_cast<unsigned>((g.warps + NW - 1) / NW);
     conv1d_bwd_kernel<T, K, ACT>
-        <<<ctas, NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg), g.warps);
+        <<<ctas, NW * 32, smem, s>>>(p, m, g.seg, static_cast<int>(g.nseg), g.warps,
+                                     static_cast<int>(debug_withhold(SSD_DEBUG_CONV_TILE)));
     return cudaGetLastError();
 }
 
