@@ -732,8 +732,8 @@ const char* ssd_version(void);
  * one hand-off, so the consumers' bounded waits run out and the kernel reports
  * SSD_ERR_TIMEOUT through its status word instead of hanging (no fault, no
  * trap).  `what` = SSD_DEBUG_CONV_TILE: the convolution's producer stops before
- * tile `index`, and the first warp of its gradient leaves out batch `index` of its
- * segment; SSD_DEBUG_FWD_CARRY: the single-pass forward does not publish the
+ * tile `index`, and the first warp of its gradient leaves out batch `index` (0
+ * to 2) of its segment; SSD_DEBUG_FWD_CARRY: the single-pass forward does not publish the
  * state leaving run `index` (a run is the group of up to four consecutive
  * 128-token tiles one cluster of CTAs takes; the next run's wait gives up
  * after about a second; SSD_FLAG_SINGLE_PASS only); SSD_DEBUG_SCAN_DECAYS: the

@@ -21,6 +21,7 @@
 // us per token and about 17 us for its start, its end and the sums; issue slots
 // are 57 % busy (48 instructions per channel pair and token), the FMA pipe 51 %,
 // the special-function pipe 39 %.
+#include <type_traits>
 #include "mixers.h"
 #include "rows_tma.cuh"
 #include "tcgen05.cuh"
@@ -83,7 +84,7 @@ struct ConvBwdMaps {
 };
 
 // segments of seg tokens (a multiple of kSegUnit), nseg per (batch, channel block).
-// `withhold` >= 0 makes the first warp leave that batch out (a test of the bounded
+// `withhold` = 0, 1, 2 makes the first warp leave that batch out (a test of the bounded
 // wait); -1 in normal use.
 template <typename T, int K, bool ACT>
 __global__ void __launch_bounds__(NW * 32, kPerSm)
@@ -114,9 +115,7 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
     const int total = nb + (K > 1 ? 1 : 0);
 
     uint8_t* ring = smem + warp * kWarpBytes<T>;
-    const int skipped = wi == 0 ? withhold : -1;
     auto load = [&](int n) {
-        if (n == skipped) return;
         const uint32_t dst = tc::smem_u32(ring) + (n % R) * 2 * kTile, bar = tc::smem_u32(&loaded[warp][n % R]);
         const int t = static_cast<int>(ta + static_cast<int64_t>(n) * TB);
         tc::mbar_expect_tx(bar, 2 * kTile);
@@ -124,7 +123,8 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         tc::tma_load_rows(dst + kTile, &maps.dy, bar, static_cast<int>(c0), t, static_cast<int>(b));
     };
     if (lane == 0)
-        for (int n = 0; n < R && n < total; ++n) load(n);
+        for (int n = 0; n < R && n < total; ++n)
+            if (n != withhold || wi > 0) load(n);
 
     float2 w[K], dw[K], bias = dup(0.0f), db = dup(0.0f);
 #pragma unroll
@@ -172,6 +172,37 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         for (int k = 1; k < K; ++k) g = fma2(w[k], dv[KM + j - k], g);
         return g;
     };
+    // Eight tokens from t on of a segment's first batch or its last (the halo), or with
+    // tokens past the sequence's end (`past`): these have no gradient and no share in
+    // the sums, whatever the inputs before them (0 times an infinite one is not 0).
+    auto edge = [&](uint8_t* tile, int64_t t, int n, auto past) {
+        constexpr bool PAST = decltype(past)::value;
+        const bool halo = n == nb;
+#pragma unroll
+        for (int j = 0; j < SB; ++j) {
+            token(tile, j);
+            const bool end = PAST && t + j >= L;
+            if (end) dv[KM + j] = dup(0.0f);
+            if (!halo && !end) sums(j);
+            float2 g = input_gradient(j);
+            const int64_t f = t + j - L;
+            if (PAST && f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
+                g.x += p.d_final[(b * Cn + c) * KM + f];
+                g.y += p.d_final[(b * Cn + c + 1) * KM + f];
+            }
+            const int64_t i = t + j - KM;
+            if (n > 0 && !halo) {
+                *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g);
+            } else if (active) {
+                if (halo ? (j < KM && i < te) : i >= ta) {
+                    if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g);
+                } else if (n == 0 && i < 0 && p.d_init) {
+                    p.d_init[(b * Cn + c) * KM + (KM + i)] = g.x;
+                    p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g.y;
+                }
+            }
+        }
+    };
     int late = total;  // the batch whose wait gave up
     for (int n = 0; n < total; ++n) {
         uint8_t* tile = ring + (n % R) * 2 * kTile + lane * sizeof(Raw);
@@ -191,33 +222,10 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
                     sums(j);
                     *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(input_gradient(j));
                 }
+            } else if (t0 + o + SB <= L) {
+                edge(tile, t0 + o, n, std::false_type());
             } else {
-                const int64_t t = t0 + o;
-#pragma unroll
-                for (int j = 0; j < SB; ++j) {
-                    token(tile, j);
-                    // no gradient past the sequence's end, whatever the inputs before it, and no
-                    // share of the sums (0 times an infinite input is not 0)
-                    if (t + j >= L) dv[KM + j] = dup(0.0f);
-                    else if (!halo) sums(j);
-                    float2 g = input_gradient(j);
-                    const int64_t f = t + j - L;
-                    if (f >= 0 && f < KM && p.d_final && active) {  // inputs the final state repeats
-                        g.x += p.d_final[(b * Cn + c) * KM + f];
-                        g.y += p.d_final[(b * Cn + c + 1) * KM + f];
-                    }
-                    const int64_t i = t + j - KM;
-                    if (n > 0 && !halo) {
-                        *reinterpret_cast<Raw*>(tile + j * kRowBytes<T>) = P::narrow(g);
-                    } else if (active) {
-                        if (halo ? (j < KM && i < te) : i >= ta) {
-                            if (i < L) *reinterpret_cast<Raw*>(dxb + i * Cn) = P::narrow(g);
-                        } else if (n == 0 && i < 0 && p.d_init) {
-                            p.d_init[(b * Cn + c) * KM + (KM + i)] = g.x;
-                            p.d_init[(b * Cn + c + 1) * KM + (KM + i)] = g.y;
-                        }
-                    }
-                }
+                edge(tile, t0 + o, n, std::true_type());
             }
 #pragma unroll
             for (int k = 0; k < KM; ++k) {
@@ -243,7 +251,7 @@ __global__ void __launch_bounds__(NW * 32, kPerSm)
         // the copies in flight land (bounded) before the warp leaves its shared memory
         const int issued = late > 0 ? late - 1 + R : R;
         for (int n = late; n < issued && n < total; ++n)
-            if (n != skipped) wait_loaded(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
+            wait_loaded(tc::smem_u32(&loaded[warp][n % R]), (n / R) & 1);
         if (lane == 0) atomicAdd(&g_conv_bwd_gave_up, 1u);
         return;
     }

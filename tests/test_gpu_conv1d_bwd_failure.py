@@ -36,10 +36,9 @@ print("TIMEOUT-OK")
 """
 
 
-@pytest.mark.parametrize("dtype,batch", [("bfloat16", 0), ("bfloat16", 1), ("float32", 5)])
+@pytest.mark.parametrize("dtype,batch", [("bfloat16", 0), ("bfloat16", 1), ("float32", 2)])
 def test_a_withheld_batch_times_out(dtype, batch):
-    """The first batch, one with a store before it, and one whose place in the ring has
-    been used before (segments have at least six batches here)."""
+    """The first batch and later ones, whose segment has stores on their way by then."""
     code = f"ROOT = {ROOT!r}\nDTYPE = {dtype!r}\nBATCH = {batch}\n" + SCRIPT
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=180)
     assert r.returncode == 0 and "TIMEOUT-OK" in r.stdout, r.stdout + r.stderr
