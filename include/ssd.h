@@ -519,9 +519,11 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
  * state rounded once.  A token's rounding errors are relative to what it keeps of
  * the state, a_t |h_{t-1}|, and to its input, however small a_t is.  After an
  * infinite state (an infinite input or carried state, an overflow) the states read
- * infinite or NaN up to the next restart.  A gate_x below -41.5 counts as -41.5 (i = 2^-60); a gate_a
- * below -87, or below about -46 next to such a gate_x, as shut (r = 0, the token
- * changes nothing).  Results do not depend on timing (no atomics).
+ * infinite or NaN up to the next restart.  A gate_x below -41.5 counts as -41.5 (i
+ * = 2^-60).  Where gate_a - log(1 + e^-gate_x) lies below about -87 (gate_a alone for
+ * an open gate_x, both together for a shut one) the token counts as shut: r = i = 0,
+ * it changes nothing (it would have added less than 1e-18 sqrt(scale
+ * softplus(decay)) |x|).  Results do not depend on timing (no atomics).
  * Supported: channels a multiple of 8 (bf16) or 4 (fp32), batch <= 65535,
  *   seqlen < 2^31 (else SSD_ERR_UNSUPPORTED); scale > 0 and finite; every
  *   pointer but reset 16-byte aligned (else SSD_ERR_INVALID_ARG).  Outputs

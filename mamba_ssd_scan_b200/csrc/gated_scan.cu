@@ -127,8 +127,8 @@ constexpr uint32_t kLeastX = 0xC226C226u;  // -41.5: e^41.5 < 2^60
 // 1 / ((1 + e^-a)(1 + e^-x)) times the other factor (a reciprocal each would
 // make five special-function results per element, close to what the pipe
 // gives in the time the bytes take).  e^-x is cut off at 2^60 (i is then off by
-// 2^-60); with a below about -46 the product may overflow, its reciprocal is 0
-// and r = i = 0: the gate counts as shut, where r < 2^-66.
+// 2^-60).  Where the product passes 2^126 its reciprocal is 0 and r = i = 0: the token
+// counts as shut, where sqrt(r) i, the size of what it adds, is below 2^-62.
 template <bool EXACT>
 __device__ __forceinline__ void sigmas(float2 ga, float2 gx, float2& r, float2& i) {
     const float2 one = dup(1.0f);
