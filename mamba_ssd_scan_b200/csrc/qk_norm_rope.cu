@@ -437,14 +437,15 @@ __global__ void __launch_bounds__(TPB, 2)
                 sum += __shfl_xor_sync(0xffffffffu, sum, o);
                 m += __shfl_xor_sync(0xffffffffu, m, o);
             }
-            // (a lane without a unit holds an earlier one's values: it adds 0 to the sums)
-            const float s1 = live ? rsqrtf(fmaf(sum, inv_d, p.eps)) : 0.0f;
+            const float s1 = rsqrtf(fmaf(sum, inv_d, p.eps));
             const float2 inv = dup(s1), k = dup(-s1 * s1 * m * inv_d);
 #pragma unroll
             for (int j = 0; j < N / 2; ++j) {
                 const float2 n0 = mul2(lo[j], inv), n1 = mul2(hi[j], inv);
-                acc0[j] = fma2(e0[j], n0, acc0[j]);
-                acc1[j] = fma2(e1[j], n1, acc1[j]);
+                if (live) {  // (a lane without a unit holds an earlier one's values)
+                    acc0[j] = fma2(e0[j], n0, acc0[j]);
+                    acc1[j] = fma2(e1[j], n1, acc1[j]);
+                }
                 e0[j] = fma2(n0, k, mul2(g0[j], inv));
                 e1[j] = fma2(n1, k, mul2(g1[j], inv));
             }

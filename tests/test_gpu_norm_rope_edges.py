@@ -38,3 +38,23 @@ def test_angles_of_high_frequencies_at_far_positions(adjacent):
     s = 1.0 / np.sqrt((v * v).mean(-1, keepdims=True) + 1e-5)
     turned = ang * s * (size + np.abs(v) * s * s * (size * np.abs(v)).mean(-1, keepdims=True))
     assert (np.abs(got - r["dv"]) <= r["e_dv"] + turned + 2.0 ** -24 * np.abs(r["dv"])).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("L", [37, 20011])
+def test_an_infinite_gradient_gives_an_infinite_weight_gradient(dtype, L):
+    """dq_weight[j] sums the incoming gradients of element j times positive values: where
+    one of them is infinite, or all are, the sum is infinite, also where a CTA's last
+    round has lanes without a head.  The other elements are what they are without."""
+    g = torch.Generator().manual_seed(L)
+    q = (torch.rand((1, L, 5, 128), generator=g) + 0.5).to(dtype).to(DEV)
+    d = torch.randn((1, L, 5, 128), generator=g).to(dtype).to(DEV)
+    clean = ssd.ssd_qk_norm_rope_bwd(q, None, None, None, None, d, None)["dq_weight"]
+    rest = [j for j in range(128) if j not in (9, 77)]
+    for everywhere in (True, False):
+        dirty = d.clone()
+        dirty[:, :, :, 9] = float("inf") if everywhere else dirty[:, :, :, 9]
+        dirty[:, L - 1, 4, 77] = float("-inf")
+        got = ssd.ssd_qk_norm_rope_bwd(q, None, None, None, None, dirty, None)["dq_weight"]
+        assert got[77] == float("-inf") and (not everywhere or got[9] == float("inf"))
+        assert torch.equal(got[rest], clean[rest])
