@@ -271,15 +271,17 @@ __device__ __forceinline__ float2 apply(float4 m, bool restart, float2 h) {
     return restart ? H : fma2(make_float2(m.x, m.y), h, H);
 }
 
+// f(restarts): a group without one takes code without its selects
+template <bool RESET, typename F> __device__ __forceinline__ void by_restarts(uint32_t rst, F f) {
+    if (RESET && rst != 0) f(std::true_type());
+    else f(std::false_type());
+}
 // f(slow, restarts) for the two properties of a group that change its code
 template <bool RESET, typename F> __device__ __forceinline__ void by_group(bool slow, uint32_t rst, F f) {
-    if (RESET && rst != 0) {
-        if (slow) f(std::true_type(), std::true_type());
-        else f(std::false_type(), std::true_type());
-    } else {
-        if (slow) f(std::true_type(), std::false_type());
-        else f(std::false_type(), std::false_type());
-    }
+    by_restarts<RESET>(rst, [&](auto restarts) {
+        if (slow) f(std::true_type(), restarts);
+        else f(std::false_type(), restarts);
+    });
 }
 
 struct Exchange {
@@ -338,14 +340,105 @@ struct ScanMaps {
     CUtensorMap x, gate_a, gate_x, y;
 };
 
+template <typename T> constexpr int kRingBytes = 2 * 3 * NW * kFwdTokens<T> * kRowBytes<T>;
+
+// A compute warp's groups, one per round: t is its first, reset the batch row's
+// restarts, states the kept states of the lane's channels (or null).
+template <typename T, bool RESET, bool SLOW>
+__device__ __forceinline__ void scan_groups(float2 k, const uint8_t* reset, float* states, int64_t L, int64_t C,
+                                            int64_t t, int64_t round, int rounds) {
+    constexpr bool EXACT = sizeof(T) == 4;
+    constexpr int ST = 2, TPT = kFwdTokens<T>, TB = TPT * kRowBytes<T>, CB = NW * TB;
+    using Raw = typename Pair<T>::Raw;
+    extern __shared__ __align__(128) uint8_t ring[];
+    Exchange& ex = *reinterpret_cast<Exchange*>(ring + kRingBytes<T>);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool flag = RESET && reset_flag<TPT>(reset, 0, t, L, lane);
+    uint8_t* const mine = ring + warp * TB + lane * sizeof(Raw);
+    for (int it = 0; it < rounds; ++it, t += round) {
+        const int slot = it % ST;
+        uint8_t* src = mine + slot * 3 * CB;
+        auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * CB + j * kRowBytes<T>); };
+        uint32_t rst = 0;
+        if constexpr (RESET) {
+            rst = __ballot_sync(0xffffffffu, flag);
+            flag = reset_flag<TPT>(reset, 0, t + round, L, lane);
+        }
+        wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
+        // the gates and the maps from the group's start up to each token
+        float2 As[TPT], Hs[TPT];
+        float2 A = dup(1.0f), H = dup(0.0f);
+        by_restarts<RESET>(rst, [&](auto restarts) {
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
+                float2 r, i, ga = read_gates(*at(2, j), kLeastA);
+                if (rs) ga = dup(0.0f);  // not used: whatever it holds
+                sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r, i);
+                As[j] = decays<EXACT, SLOW>(mul2(k, r));  // (the token's multiplier, then its map)
+                float2 n = input_weight<SLOW, true>(far_of<SLOW>(As[j]), As[j]);
+                if (rs) n = dup(1.0f);
+                Hs[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
+            }
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
+                const Far far = far_of<SLOW>(As[j]);
+                H = rs ? Hs[j] : step(far, As[j], H, Hs[j]);
+                A = rs ? dup(0.0f) : keep(far, As[j], A);
+                As[j] = A;
+                Hs[j] = H;
+            }
+        });
+        if (t + TPT > L) {  // the group's map is its last token's
+            A = dup(1.0f);
+            H = dup(0.0f);
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) {
+                A = t + j < L ? As[j] : A;
+                H = t + j < L ? Hs[j] : H;
+            }
+        }
+        ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
+        if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
+        // the outputs, over gate_a's tile; the ninth warp's wait on its cluster is
+        // bounded and it always arrives
+        wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
+        const float2 h = ex.entering[warp][lane];
+        // (a kept state's token starts a group)
+        if (states && t < L && t % kInterval == 0)
+            *reinterpret_cast<float2*>(states + t / kInterval * C) = h;
+        if (RESET && rst != 0) {
+            const int from = __ffs(static_cast<int>(rst)) - 1;  // where h is dropped
+#pragma unroll
+            for (int j = 0; j < TPT; ++j)
+                *at(2, j) = Pair<T>::narrow(j >= from ? Hs[j] : fma2(As[j], h, Hs[j]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < TPT; ++j) *at(2, j) = Pair<T>::narrow(fma2(As[j], h, Hs[j]));
+        }
+        tc::fence_smem_async();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
+    }
+}
+// The same as a function that is called: next to the other decays' code the compiler
+// found worse schedules for either (b1 L65536 C1536 bf16 227 us, by calls 221; b6
+// L4096 C4736 at decays from 0.3 on 199, by calls 193).  With restarts it is the
+// other way round (b8 L4096 C2048 149 us by calls, 145 without).
+template <typename T, bool SLOW, typename... Args> __device__ __noinline__ void call_scan_groups(Args... args) {
+    scan_groups<T, false, SLOW>(args...);
+}
+
 template <typename T, bool RESET>
 __global__ void __launch_bounds__(kThreads, 3)
     gated_scan_kernel(GatedScanParams p, const __grid_constant__ ScanMaps maps, int cl, int withhold) {
-    constexpr bool EXACT = sizeof(T) == 4;
     constexpr int ST = 2, TPT = kFwdTokens<T>, TILE = NW * TPT, TB = TPT * kRowBytes<T>, CB = NW * TB;
     using Raw = typename Pair<T>::Raw;
     extern __shared__ __align__(128) uint8_t ring[];    // [ST][3] tiles: x, gate_x, gate_a (then y)
-    __shared__ Exchange ex;
+    Exchange& ex = *reinterpret_cast<Exchange*>(ring + kRingBytes<T>);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t C = p.channels, L = p.seqlen, b = blockIdx.y;
     const int rank = static_cast<int>(blockIdx.x) % cl;
@@ -441,77 +534,15 @@ __global__ void __launch_bounds__(kThreads, 3)
         const int64_t nst = (L + kInterval - 1) / kInterval;
         const float2 k = decay_rates(p, c, active);
         const bool slow = __all_sync(0xffffffffu, k.x >= -0.25f && k.y >= -0.25f);
-        int64_t t = first + warp * TPT;  // the group's first token
-        bool flag = RESET && reset_flag<TPT>(p.reset, b, t, L, lane);
-        uint8_t* const mine = ring + warp * TB + lane * sizeof(Raw);
-        for (int it = 0; it < rounds; ++it, t += round) {
-            const int slot = it % ST;
-            uint8_t* src = mine + slot * 3 * CB;
-            auto at = [&](int tile, int j) { return reinterpret_cast<Raw*>(src + tile * CB + j * kRowBytes<T>); };
-            uint32_t rst = 0;
-            if constexpr (RESET) {
-                rst = __ballot_sync(0xffffffffu, flag);
-                flag = reset_flag<TPT>(p.reset, b, t + round, L, lane);
-            }
-            wait_phase(tc::smem_u32(&ex.loaded[slot]), (it / ST) & 1, kOwnProbes, &ex.abort);
-            // the gates and the maps from the group's start up to each token
-            float2 As[TPT], Hs[TPT];
-            float2 A = dup(1.0f), H = dup(0.0f);
-            by_group<RESET>(slow, rst, [&](auto is_slow, auto restarts) {
-                constexpr bool SLOW = decltype(is_slow)::value;
-#pragma unroll
-                for (int j = 0; j < TPT; ++j) {
-                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    float2 r, i, ga = read_gates(*at(2, j), kLeastA);
-                    if (rs) ga = dup(0.0f);  // not used: whatever it holds
-                    sigmas<EXACT>(ga, read_gates(*at(1, j), kLeastX), r, i);
-                    As[j] = decays<EXACT, SLOW>(mul2(k, r));  // (the token's multiplier, then its map)
-                    float2 n = input_weight<SLOW, true>(far_of<SLOW>(As[j]), As[j]);
-                    if (rs) n = dup(1.0f);
-                    Hs[j] = mul2(mul2(n, i), Pair<T>::widen(*at(0, j)));
-                }
-#pragma unroll
-                for (int j = 0; j < TPT; ++j) {
-                    const bool rs = decltype(restarts)::value && ((rst >> j) & 1);
-                    const Far far = far_of<SLOW>(As[j]);
-                    H = rs ? Hs[j] : step(far, As[j], H, Hs[j]);
-                    A = rs ? dup(0.0f) : keep(far, As[j], A);
-                    As[j] = A;
-                    Hs[j] = H;
-                }
-            });
-            if (t + TPT > L) {  // the group's map is its last token's
-                A = dup(1.0f);
-                H = dup(0.0f);
-#pragma unroll
-                for (int j = 0; j < TPT; ++j) {
-                    A = t + j < L ? As[j] : A;
-                    H = t + j < L ? Hs[j] : H;
-                }
-            }
-            ex.group_map[warp][lane] = make_float4(A.x, A.y, H.x, H.y);
-            if (RESET && lane == 0) ex.group_rst[warp] = rst != 0;
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.maps_ready));
-            // the outputs, over gate_a's tile; the ninth warp's wait on its cluster is
-            // bounded and it always arrives
-            wait_phase(tc::smem_u32(&ex.states_ready), it & 1, kOwnProbes, &ex.abort);
-            const float2 h = ex.entering[warp][lane];
-            // (a kept state's token starts a group)
-            if (p.states && active && t < L && t % kInterval == 0)
-                *reinterpret_cast<float2*>(p.states + (b * nst + t / kInterval) * C + c) = h;
-            if (RESET && rst != 0) {
-                const int from = __ffs(static_cast<int>(rst)) - 1;  // where h is dropped
-#pragma unroll
-                for (int j = 0; j < TPT; ++j)
-                    *at(2, j) = Pair<T>::narrow(j >= from ? Hs[j] : fma2(As[j], h, Hs[j]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < TPT; ++j) *at(2, j) = Pair<T>::narrow(fma2(As[j], h, Hs[j]));
-            }
-            tc::fence_smem_async();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(tc::smem_u32(&ex.outputs_ready));
+        const uint8_t* reset = RESET ? p.reset + b * L : nullptr;
+        float* states = p.states && active ? p.states + b * nst * C + c : nullptr;
+        const int64_t t = first + warp * TPT;
+        if constexpr (RESET) {
+            if (slow) scan_groups<T, true, true>(k, reset, states, L, C, t, round, rounds);
+            else scan_groups<T, true, false>(k, reset, states, L, C, t, round, rounds);
+        } else {
+            if (slow) call_scan_groups<T, true>(k, reset, states, L, C, t, round, rounds);
+            else call_scan_groups<T, false>(k, reset, states, L, C, t, round, rounds);
         }
     }
     __syncthreads();
@@ -960,7 +991,7 @@ size_t gated_scan_bwd_partial_bytes(int64_t batch, int64_t, int64_t channels) {
 
 template <typename T> cudaError_t launch_gated_scan(const GatedScanParams& p, cudaStream_t s) {
     constexpr int tile = NW * kFwdTokens<T>;
-    const size_t smem = 2 * 3 * tile * kRowBytes<T>;
+    const size_t smem = kRingBytes<T> + sizeof(Exchange);
     ScanMaps m;
     const std::pair<CUtensorMap*, const void*> arrays[] = {
         {&m.x, p.x}, {&m.gate_a, p.gate_a}, {&m.gate_x, p.gate_x}, {&m.y, p.y}};
