@@ -521,9 +521,10 @@ ssd_status ssd_conv1d_update(const ssd_conv1d_update_args* args, void* stream);
  * infinite state (an infinite input or carried state, an overflow) the states read
  * infinite or NaN up to the next restart.  A gate_x below -41.5 counts as -41.5 (i
  * = 2^-60).  Where gate_a - log(1 + e^-gate_x) lies below about -87 (gate_a alone for
- * an open gate_x, both together for a shut one) the token counts as shut: r = i = 0,
- * it changes nothing (it would have added less than 1e-18 sqrt(scale
- * softplus(decay)) |x|).  Results do not depend on timing (no atomics).
+ * an open gate_x, both together for a shut one), or 1 - a_t^2 below 2^-126, the token
+ * counts as shut: it changes nothing (it would have added less than 1e-18 |x| times
+ * the larger of 1 and sqrt(scale softplus(decay))).  Results do not depend on timing
+ * (no atomics).
  * Supported: channels a multiple of 8 (bf16) or 4 (fp32), batch <= 65535,
  *   seqlen < 2^31 (else SSD_ERR_UNSUPPORTED); scale > 0 and finite; every
  *   pointer but reset 16-byte aligned (else SSD_ERR_INVALID_ARG).  Outputs

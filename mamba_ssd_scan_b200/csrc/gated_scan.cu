@@ -201,6 +201,8 @@ template <bool SLOW, bool DIRECT> __device__ __forceinline__ float2 input_weight
     const float2 n2 = one_less_square<SLOW, DIRECT>(far, m);
     return make_float2(sqrt_approx(n2.x), sqrt_approx(n2.y));
 }
+// the least 1 - a^2 whose root is formed, 2^-126
+constexpr float kLeastSquare = 1.17549435e-38f;
 // -scale * softplus(decay) of a pair of channels (0 outside them)
 __device__ __forceinline__ float2 decay_rates(const GatedScanParams& p, int64_t c, bool active) {
     return active ? make_float2(-p.scale * softplus_f32(p.decay[c]), -p.scale * softplus_f32(p.decay[c + 1]))
@@ -775,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                     // n and 1 / n from one reciprocal root; a decay of exactly 1 (n = 0)
                     // gives a finite dla, times la = 0
                     const float2 n2 = one_less_square<SLOW, false>(far, m[j]);
-                    const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, 1e-36f)),
-                                                  rsqrt_approx(max_nan(n2.y, 1e-36f)));
+                    const float2 rn = make_float2(rsqrt_approx(max_nan(n2.x, kLeastSquare)),
+                                                  rsqrt_approx(max_nan(n2.y, kLeastSquare)));
                     const float2 n = rs ? dup(1.0f) : mul2(n2, rn);
                     const float2 dx = mul2(mul2(g, n), i[j]);
                     const float2 dgx = mul2(dx, fma2(ix, dup(-1.0f), x));

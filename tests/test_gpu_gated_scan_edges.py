@@ -87,3 +87,31 @@ def test_an_infinite_end_is_the_final_state(dtype, decay):
         # dx = g n i, g infinite
         assert torch.isinf(o["dx"][0, L - 1, 3]) and o["dx"][0, L - 1, 3] > 0, L
         assert torch.isfinite(o["dx"][0, :, [0, 1, 4, 6, 7]]).all(), L
+
+
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_nearly_shut_gates_relative_to_what_they_add(dtype):
+    """Down to where a gate counts as shut a token adds sqrt(2 scale softplus(decay) r) i x
+    with r as small as e^-86: outputs of 1e-18 and their gradients keep their relative
+    accuracy.  A bf16 gate's e^-v is off by up to half an ulp of v log2 e in the
+    exponent: 2^-19 ln 2 of itself from 2^5 on, 2^-18 ln 2 from 2^6 on; half of that in
+    the square root."""
+    ga = torch.arange(-86.0, -30.0, 4.0)
+    L, C = ga.numel(), 8
+    x = torch.linspace(1, 2, L)[None, :, None].repeat(1, 1, C).to(dtype)
+    gx = torch.full((1, L, C), 6.0).to(dtype)
+    gav = ga[None, :, None].repeat(1, 1, C).to(dtype)
+    dec = torch.linspace(-3, 3, C)
+    dy = torch.ones(1, L, C, dtype=dtype)
+    # a token per call: the states before it would hide it
+    for t in range(L):
+        one = [v[:, t:t + 1].contiguous() for v in (x, gav, gx)]
+        g = [v.to(DEV) for v in one] + [dec.to(DEV)]
+        y, st = ssd.ssd_gated_scan(*g, return_states=True)
+        ref = om.gated_scan(*one, dec)
+        more = 2.0 ** -18 * 0.7 if dtype is BF else 0.0
+        within(y, ref["y"], ref["e_y"] + more * abs(ref["y"]), f"y at gate {ga[t]}")
+        o = ssd.ssd_gated_scan_bwd(*g, dy[:, t:t + 1].to(DEV), st)
+        ref = om.gated_scan_bwd(*one, dec, dy[:, t:t + 1])
+        for k in ("dx", "dgate_x"):
+            within(o[k], ref[k], ref["e_" + k] + more * abs(ref[k]), f"{k} at gate {ga[t]}")
