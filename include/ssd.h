@@ -626,7 +626,8 @@ ssd_status ssd_gated_state_update(const ssd_gated_state_update_args* args, void*
  * (2 pi), are formed in two fp64 parts and held as a 64-bit fraction, so that whole
  * turns drop out of the product with the position exactly: the angle is off by less
  * than 2^-25 of a turn at positions up to 2^31, whatever inv_freq; cosine and sine
- * are fp32.
+ * are fp32.  So is the mean: a head whose squares leave the fp32 range (elements
+ * above about 1e18, or all below 1e-19 with eps = 0) is not normalised.
  * Layouts: q, q_out: batch * seqlen tokens q_stride / q_out_stride elements
  *   apart, each with q_heads dense heads of headdim elements, dtype; k, k_out
  *   alike (NULL with k_heads = 0).  So slices of one packed row per token are

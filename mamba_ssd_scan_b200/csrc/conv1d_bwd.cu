@@ -16,11 +16,11 @@
 // kernel adds the rows in order.
 //
 // Measured (B200, L2 flushed; share of the measured copy bandwidth over the
-// call's least bytes), K 4 with SiLU: bf16 b1 L65536 C5376 373 us (88 %), b8 L4096
-// C2304 96 us (73 %); fp32 b8 L4096 C1536 115 us (82 %).  A segment costs 0.15
-// us per token and about 17 us for its start, its end and the sums; issue slots
-// are 57 % busy (48 instructions per channel pair and token), the FMA pipe 51 %,
-// the special-function pipe 39 %.
+// call's least bytes), K 4 with SiLU: bf16 b1 L65536 C5376 378 us (87 %), b8 L4096
+// C2304 97 us (72 %); fp32 b8 L4096 C1536 119 us (79 %).  A call costs 0.15 us per
+// token of a segment and about 17 us besides (the launch, filling the ring, the
+// segments' ends, the sums' kernel); issue slots are 55 % busy (44 instructions per
+// channel pair and token), the FMA pipe 53 %, the special-function pipe 41 %.
 #include <type_traits>
 #include "mixers.h"
 #include "rows_tma.cuh"
@@ -274,8 +274,10 @@ __global__ void __launch_bounds__(kSumWarps * 32) conv1d_bwd_finish_kernel(ConvB
 }
 
 // Segments: the number, up to one per 32 tokens, with the least waves x (tokens
-// of a segment + the tokens' worth of its start, end and sums, about 16), at
-// the warps the device holds at once.
+// of a segment + the batch it loads past its end, 16), at the warps the device
+// holds at once.  The addend hardly matters, since the least is nearly always one
+// full wave: 1, 16, 64 and 113 measured the same at ten sizes from b1 L1030 C64 to
+// b1 L65536 C5376.
 struct ConvGrid {
     int64_t seg, nseg, warps;
 };

@@ -11,9 +11,9 @@
 // inputs are read once.
 //
 // A compute warp takes one group of tokens of 64 channels (a pair per lane);
-// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens;
-// 32 in the fp32 forward), and the CTAs of a cluster consecutive tiles.  A ninth warp composes the
-// tile's map, sends it to the cluster's CTAs through distributed shared memory
+// the 8 compute warps of a CTA take consecutive groups (a tile of 64 tokens; 32 in
+// the fp32 forward), and the CTAs of a cluster consecutive tiles.  A ninth warp
+// composes the tile's map, sends it to the cluster's CTAs through distributed shared memory
 // (asynchronous stores that complete on the receiver's mbarrier), and hands
 // each group its entering state.  The order of composition is fixed, so
 // results do not depend on timing; there is no workspace and no wait on another
@@ -21,17 +21,23 @@
 // flag, finishes without waiting, and the call's status reads SSD_ERR_TIMEOUT.
 //
 // Measured (B200, L2 flushed; share of the measured copy bandwidth over the
-// call's least bytes).  Forward, bf16: b6 L4096 C4736 172 us (84 %), b8 L4096
-// C2048 127 us (66 %), with restarts 145; b1 L65536 C1536 227 us (55 %); fp32: b8
-// L4096 C2048 197 us (85 %).  Gradient, bf16: b4 L4096 C4736 225 us (75 %), b8
-// L4096 C2048 223 us (65 %), with restarts 250; b1 L65536 C1536 421 us (52 %).
-// Groups of 16 tokens at two CTAs per SM measured 220 us at b6 C4736, groups of
-// four at four CTAs 203.  Where the CTAs fill the SMs evenly the
-// forward is bound by its instructions (55 per channel pair and token; issue
-// slots 55 % busy, the special-function pipe 62 %) as much as by its bytes, and
-// the gradient by its own (issue 54 %, FMA pipe 46 %, at two CTAs per SM).  b8 C2048
-// is 256 CTAs on 148 SMs, a third of which take one where the others take two;
-// halves of the sequence in clusters of two cost more than they even out.
+// call's least bytes).  Forward, bf16: b6 L4096 C4736 174 us (83 %), b8 L4096
+// C2048 127 us (66 %), with eight restarts a row 150; b1 L65536 C1536 227 us (55
+// %); fp32: b8 L4096 C2048 199 us (84 %).  Gradient, bf16: b4 L4096 C4736 226 us (75
+// %), b8 L4096 C2048 224 us (65 %), with eight restarts a row 263; b1 L65536 C1536
+// 421 us (52 %); fp32: b8 L4096 C2048 390 us (75 %).  These have the usual decays,
+// 0.9 to 0.999 at the open gate.  Where a warp's channels reach decays below e^-1/4
+// (drawn from 0.3 to 0.999) its other code runs: b8 L4096 C2048 bf16 145 us, with
+// restarts 172, the gradient 276 and 314; b1 L65536 C1536 262 and 511; fp32 213 and
+// 421.  Groups of 16 tokens at two CTAs per SM measured 220 us at b6 C4736, groups of
+// four at four CTAs 203 (172 then).  Where the CTAs fill the SMs evenly the forward
+// is bound by its instructions (55 per channel pair and token; issue slots 54 % busy,
+// the special-function pipe 63 %) as much as by its bytes.  Neither binds the
+// gradient: at b8 C2048 its bytes take 146 us and its instructions 120 (issue 54 %);
+// it waits, with 14.7 warps on an SM, which its 96 registers a thread allow (9
+// warps, two CTAs; it spills 8 to 16 bytes there, the forward with restarts 16 at
+// 72).  b8 C2048 is 256 CTAs on 148 SMs, a third of which take one where the others
+// take two; halves of the sequence in clusters of two cost more than they even out.
 // Long sequences of few channels wait for the exchange, once per round.
 #include <atomic>
 #include <type_traits>
@@ -825,8 +831,8 @@ __global__ void __launch_bounds__(kSumWarps * 32) gated_scan_finish_kernel(Gated
 // The decode step: a thread takes 4 channels of R batch rows, so that the
 // channels' softplus is formed once for all of them and R rows' loads are in
 // flight together.  Bandwidth-bound at large batches (the state in and out, four
-// inputs and outputs; fp32 b512 C5120 18.4 us between events, 52 MB that mostly
-// stay in L2); a small one is its launch, and consecutive steps overlap theirs
+// inputs and outputs; fp32 b512 C5120 17 to 18 us between events after an L2 flush, 7.8
+// back to back from L2, its 63 MB 9.7); a small one is its launch, and consecutive steps overlap theirs
 // by programmatic dependent launch (bf16 b256 C5120 8 us a step, one row of
 // 1536 channels the same).
 constexpr int kUpdateThreads = 128;

@@ -17,9 +17,10 @@
 // rows 101 us (83 %), b4 L4096 32 + 8 heads of 128 62 us (84 %); fp32: b4 L4096
 // 32 + 8 heads of 64, adjacent pairs, 61 us (85 %).  Issue slots are 73 % busy (18
 // instructions per element), so instructions and bytes bind about equally.
-// Gradient, bf16: b4 L4096 32 + 8 heads of 128 104 us (75 %), heads of 64 59 us
-// (66 %); issue 59 %, and without its arithmetic the same loop still takes 99 us:
-// the loads in flight of two CTAs per SM bind it.  Two units in flight per lane
+// Gradient, bf16: b4 L4096 32 + 8 heads of 128 101 us (77 %), heads of 64 59 us
+// (66 %); issue 58 %, and without its arithmetic the same loop still takes 99 us:
+// the loads in flight of two CTAs per SM bind it.  The forward spills 12 bytes for
+// adjacent bf16 pairs at 2, 4 and 8 lanes per unit.  Two units in flight per lane
 // (126 registers) measured 115 us, three CTAs per SM (80 registers) spilled, 152.
 #include <algorithm>
 #include "mixers.h"
